@@ -55,8 +55,9 @@ enum w8_status {
   W8_ERR_LAUNCH = -5, /* the HIP runtime rejected a kernel launch or a workspace allocation */
   W8_ERR_WORKSPACE = -6, /* a workspace is smaller than required (a caller-provided one, or the
                             fixed scratch of gemm_w8a8_channel_noalloc) */
-  W8_ERR_CAPTURE = -7  /* the call would allocate its scratch while its stream is being captured
+  W8_ERR_CAPTURE = -7, /* the call would allocate its scratch while its stream is being captured
                           into a graph; nothing was enqueued */
+  W8_ERR_VALUE = -8    /* a scalar argument is out of its range or not finite */
 };
 
 enum w8_dtype { W8_BF16 = 0, W8_FP16 = 1, W8_FP32 = 2, W8_I32 = 3 };
@@ -381,6 +382,99 @@ int gemm_w8a8_asym(const int8_t* A_shifted, const float* a_params,
                    const int8_t* W, const float* w_scale,
                    const int32_t* w_sum, void* Y, int y_dtype,
                    int64_t M, int64_t N, int64_t K, void* stream);
+
+/*
+ * The norms between two blocks, the residual between them and the quantiser
+ * of the next block's activations, in one pass over the rows (page 1 section
+ * 2.3: activations are quantised online before every INT8 matmul; here where
+ * they are produced):
+ *   n = y * rsqrt(mean(y^2) + eps) * post_weight   (n = y if post_weight is NULL)
+ *   h = residual + residual_scale * (gate * n)     rounded to the 16-bit type
+ *   z = h * rsqrt(mean(h^2) + eps) * pre_weight    rounded to the 16-bit type
+ *   q, q_scale = quant_act_group(z) (scheme W8_SCHEME_BLOCK) or
+ *                quant_act_token(z) (W8_SCHEME_CHANNEL), bit for bit
+ * Means and products are fp32; the second norm reads h as stored, the
+ * quantiser z as rounded, so consumers of z and of the codes see the same
+ * activations.
+ *   y            [M][K] the block's output, bf16 or fp16 (dtype), as all the
+ *                16-bit arrays here
+ *   residual     [M][K] or NULL (nothing is added)
+ *   post_weight  [K] or NULL (no norm after the block)
+ *   gate         [K] (gate_rows 1) or [M][K] (gate_rows M) factors, or NULL
+ *   pre_weight   [K]
+ *   h            [M][K] out; may be the same array as residual or y
+ *   normed       [M][K] out (z), or NULL
+ *   q, q_scale   [M][K] int8 and [M][KB] or [M] fp32 out, or q NULL; one of
+ *                normed and q is required
+ * K <= 32768; eps > 0 (W8_ERR_VALUE).  A row whose sum of squares leaves
+ * fp32, or whose h leaves the 16-bit type, gives unspecified results.
+ */
+int norm_residual_quant(const void* y, const void* residual, const void* post_weight,
+                        const void* gate, int64_t gate_rows, float residual_scale,
+                        const void* pre_weight, float eps, int dtype, int scheme,
+                        int64_t M, int64_t K, void* h, void* normed, int8_t* q,
+                        float* q_scale, void* stream);
+
+/*
+ * The router of a mixture-of-experts layer (DeepSeek is an MoE model, page 4
+ * section 1.2), in 64-bit arithmetic, so that the choice is that of the
+ * formula and not of a rounding:
+ *   s = softmax(l) or 1 / (1 + exp(-l));  c = s + bias (bias NULL: c = s)
+ *   The E experts form n_group groups of E / n_group consecutive ones; a
+ *   group's score is the sum of its group_top (1 or 2) largest c, and the
+ *   topk_group groups of the largest score stay.  The topk experts of the
+ *   largest c in them are the token's, in that order; ties go to the lower
+ *   index everywhere.
+ *   weight = s of the expert, over the sum of the topk s if renormalise is
+ *   not 0 (0 if that sum is 0), times scale; rounded once to fp32.
+ *   logits [T][E] fp32, bf16 or fp16; bias [E] fp32 or NULL
+ *   ids [T][topk] int32 out, weights [T][topk] fp32 out
+ * An expert whose logit is -inf or NaN is masked: its s is 0, it counts in no
+ * group's score and is never chosen.  Slots that find no expert (fewer than
+ * topk are left, down to none) hold id -1 and weight 0.  +inf counts as the
+ * largest finite fp32.
+ * E <= 1024, topk <= 64 and <= topk_group * E / n_group, E % n_group == 0.
+ */
+enum w8_route_score { W8_ROUTE_SOFTMAX = 0, W8_ROUTE_SIGMOID = 1 };
+
+int moe_route_topk(const void* logits, int logits_dtype, const float* bias,
+                   int score, int64_t T, int64_t E, int topk, int n_group,
+                   int topk_group, int group_top, int renormalise, double scale,
+                   int32_t* ids, float* weights, void* stream);
+
+/*
+ * A whole mixture-of-experts layer for a few tokens (up to 64; for more,
+ * gemm_w8a8_block_grouped over expert-sorted rows), block-wise scheme, in two
+ * kernels that read the weights of the chosen experts once:
+ *   gate, up = the two halves of A[t] . W_gate_up[e]^T, as gemm_w8a8_block (fp32)
+ *   hq, hs   = the group quantiser of gate / (1 + exp(-gate)) * up, taken
+ *              from fp32 (no 16-bit rounding between)
+ *   Y[t]     = sum over j of topk_weights[t][j] * (hq . W_down[e]^T)[t],
+ *              e = topk_ids[t][j], summed in fp32 in slot order, rounded once
+ *   A [T][K] int8, a_scale [T][K/128]   (quant_act_group, norm_residual_quant)
+ *   topk_ids [T][topk] int32 DEVICE array, topk_weights [T][topk] fp32: a slot
+ *   whose id is outside 0 .. E - 1 (an expert of another GPU, a masked slot,
+ *   a padding row) adds nothing and its weight is not read; a token without
+ *   any slot gets a row of zeros; a token may name an expert twice
+ *   W_gate_up [E][2 I][K] int8 (gate rows first), gate_up_scale [E][2 I/128][K/128]
+ *   W_down    [E][K][I]   int8,                   down_scale    [E][K/128][I/128]
+ *   Y [T][K] bf16 or fp32 (y_dtype)
+ *   workspace: caller-owned device memory of moe_workspace_bytes(T, topk, I)
+ *   bytes (fewer gives W8_ERR_WORKSPACE), 256-byte aligned, with no contents
+ *   to keep; it must not be used by other work until the stream has passed
+ *   this call, so calls on different streams, or graphs that may run at the
+ *   same time, need one each.
+ * T <= 64, topk <= 16, E <= 4096, I and K multiples of 128 up to 2^17.
+ * Nothing is allocated; the call can be captured into a graph.
+ */
+int64_t moe_workspace_bytes(int64_t T, int64_t topk, int64_t I);
+
+int moe_w8a8_block(const int8_t* A, const float* a_scale, const int32_t* topk_ids,
+                   const float* topk_weights, const int8_t* W_gate_up,
+                   const float* gate_up_scale, const int8_t* W_down,
+                   const float* down_scale, void* Y, int y_dtype, int64_t T,
+                   int64_t topk, int64_t E, int64_t I, int64_t K,
+                   void* workspace, int64_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -34,6 +34,7 @@ Modules:
   routing  - top-k expert routing used to lay out the grouped GEMM inputs
   asym     - the asymmetric uint8 activation variant
   int4     - group-wise INT4 weights (packed two per byte) and the W4A16 GEMM
+  layer    - the norms with residual and gate, the router, the few-token experts
 """
 
-from . import formats, quant, gemm, routing, int4  # noqa: F401
+from . import formats, quant, gemm, routing, int4, layer  # noqa: F401

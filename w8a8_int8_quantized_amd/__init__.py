@@ -14,6 +14,9 @@ fallback: if libw8a8.so is missing, importing this package raises.
     y = linear_w8a8_block(x, wq, ws)           # quant_act_group + gemm_w8a8_block in one call
     qa, prm = quant_act_asym(x)                # asymmetric per-tensor uint8 (stored as q - 128)
     y = gemm_w8a8_asym(qa, prm, wq, ws, weight_row_sums(wq))   # per-channel weights
+    h, q, s, z = norm_residual_quant(y, w, residual=r, normed=True)   # norms, residual and quantiser in one pass
+    ids, wt = moe_route_topk(logits, 8)        # the experts of each token and their weights
+    y = moe_w8a8_block(q, s, ids, wt, w_gu, s_gu, w_dn, s_dn)   # all their products, up to 64 tokens
 """
 
 import ctypes
@@ -26,6 +29,7 @@ LIB_PATH = os.path.join(_HERE, "libw8a8.so")
 
 W8_BF16, W8_FP16, W8_FP32, W8_I32 = 0, 1, 2, 3
 W8_SCHEME_BLOCK, W8_SCHEME_CHANNEL = 0, 1
+W8_ROUTE_SOFTMAX, W8_ROUTE_SIGMOID = 0, 1
 GROUP = 128
 
 _FUNCS = {
@@ -85,6 +89,15 @@ _FUNCS = {
     "linear_w8a8_channel": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
                                            ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int64,
                                            ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
+    "norm_residual_quant": (ctypes.c_int, [ctypes.c_void_p] * 4 + [ctypes.c_int64, ctypes.c_float, ctypes.c_void_p,
+                                                                   ctypes.c_float, ctypes.c_int, ctypes.c_int,
+                                                                   ctypes.c_int64, ctypes.c_int64]
+                            + [ctypes.c_void_p] * 5),
+    "moe_route_topk": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
+                                      ctypes.c_int64] + [ctypes.c_int] * 5 + [ctypes.c_double] + [ctypes.c_void_p] * 3),
+    "moe_workspace_bytes": (ctypes.c_int64, [ctypes.c_int64] * 3),
+    "moe_w8a8_block": (ctypes.c_int, [ctypes.c_void_p] * 9 + [ctypes.c_int] + [ctypes.c_int64] * 5
+                       + [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
 }
 
 
@@ -102,7 +115,7 @@ def _load():
 lib = _load()
 
 
-W8_ERR_WORKSPACE, W8_ERR_CAPTURE = -6, -7
+W8_ERR_WORKSPACE, W8_ERR_CAPTURE, W8_ERR_VALUE = -6, -7, -8
 
 
 class W8Error(RuntimeError):
@@ -403,3 +416,157 @@ def gemm_w8a8_asym(A, a_params, W, w_scale, w_sum, out_dtype=torch.bfloat16, out
     _check(lib.gemm_w8a8_asym(_p(A), _p(a_params), _p(W), _p(w_scale), _p(w_sum), _p(y), _out_code(y.dtype),
                               M, N, K, _stream()), "gemm_w8a8_asym")
     return y
+
+
+# --------------------------------------------- the layer around the products
+def _like(t, name, shape, dtype, dev):
+    """t is a contiguous tensor of this shape and type on dev."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise W8Error(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.device != dev:
+        raise W8Error(f"{name} must be on {dev}")
+    if not t.is_contiguous():
+        raise W8Error(f"{name} must be contiguous")
+
+
+def _run_on(dev, what, fn, *args):
+    """The call on dev's current stream, with dev the current device."""
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream().cuda_stream), what)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, torch.cuda.current_stream().cuda_stream), what)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def norm_residual_quant(y, pre_weight, residual=None, post_weight=None, gate=None, residual_scale=1.0, eps=1e-6,
+                        scheme=W8_SCHEME_BLOCK, normed=False, out=None):
+    """The norm after a block, its gate and residual scale, the residual, the
+    norm before the next block and the quantiser, in one pass over the rows.
+
+    y [M, K] (bf16 or fp16) is the block's output; n = y, or its RMS norm with
+    post_weight [K]; h = residual + residual_scale * (gate * n), gate [K] or
+    [M, K]; z = the RMS norm of h with pre_weight [K].  Returns (h, q, s) with
+    the codes and scales of z (scheme W8_SCHEME_BLOCK: per 1x128 group,
+    W8_SCHEME_CHANNEL: per token), (h, q, s, z) with normed=True, or (h, z)
+    with scheme=None and normed=True.  out: the tensors to write, in that
+    order; h may be residual or y itself.
+    """
+    _dev(y)
+    M, K = y.shape
+    dev, dt, code = y.device, y.dtype, _act_dtype(y)
+    if scheme not in (W8_SCHEME_BLOCK, W8_SCHEME_CHANNEL, None):
+        raise W8Error(f"unknown scheme {scheme}")
+    if scheme is None and not normed:
+        raise W8Error("norm_residual_quant: nothing to return beside h (scheme None needs normed=True)")
+    _like(pre_weight, "pre_weight", (K,), dt, dev)
+    if residual is not None:
+        _like(residual, "residual", (M, K), dt, dev)
+    if post_weight is not None:
+        _like(post_weight, "post_weight", (K,), dt, dev)
+    gate_rows = 1
+    if gate is not None:
+        gate_rows = 1 if gate.dim() == 1 else M
+        _like(gate, "gate", (K,) if gate.dim() == 1 else (M, K), dt, dev)
+    want = [("h", (M, K), dt)]
+    if scheme is not None:
+        want += [("q", (M, K), torch.int8), ("scales", (M, K // GROUP) if scheme == W8_SCHEME_BLOCK else (M,),
+                                             torch.float32)]
+    if normed:
+        want += [("z", (M, K), dt)]
+    if out is None:
+        out = tuple(torch.empty(shape, dtype=t, device=dev) for _, shape, t in want)
+    else:
+        out = tuple(out)
+        if len(out) != len(want):
+            raise W8Error(f"norm_residual_quant: out must be ({', '.join(n for n, _, _ in want)})")
+        for t, (name, shape, ty) in zip(out, want):
+            _like(t, "out " + name, shape, ty, dev)
+    q, s = (out[1], out[2]) if scheme is not None else (None, None)
+    _run_on(dev, "norm_residual_quant", lib.norm_residual_quant, y.data_ptr(), _ptr(residual), _ptr(post_weight),
+            _ptr(gate), gate_rows, residual_scale, pre_weight.data_ptr(), eps, code, scheme or 0, M, K,
+            out[0].data_ptr(), _ptr(out[-1] if normed else None), _ptr(q), _ptr(s))
+    return out
+
+
+def moe_route_topk(logits, topk, bias=None, score=W8_ROUTE_SOFTMAX, n_group=1, topk_group=1, group_top=2,
+                   renormalise=True, scale=1.0, out=None):
+    """The topk experts of each token and their weights from router logits
+    [T, E] (fp32, bf16 or fp16): ids int32 [T, topk], weights fp32 [T, topk].
+
+    Scores are softmax or sigmoid (score) in 64 bits; the choice goes by score
+    + bias [E] within the topk_group best of n_group groups (by the sum of
+    their group_top largest), ties to the lower index; the weights are the
+    scores without bias, renormalised over the chosen ones and scaled.  An
+    expert with logit -inf or NaN is never chosen; slots left over hold id -1
+    and weight 0.
+    """
+    _dev(logits)
+    T, E = logits.shape
+    dev = logits.device
+    code = W8_FP32 if logits.dtype == torch.float32 else _act_dtype(logits)
+    if bias is not None:
+        _like(bias, "bias", (E,), torch.float32, dev)
+    topk = int(topk)
+    if out is None:
+        if topk < 1:
+            raise W8Error("moe_route_topk: topk must be at least 1")
+        out = (torch.empty((T, topk), dtype=torch.int32, device=dev),
+               torch.empty((T, topk), dtype=torch.float32, device=dev))
+    else:
+        _like(out[0], "out ids", (T, topk), torch.int32, dev)
+        _like(out[1], "out weights", (T, topk), torch.float32, dev)
+    _run_on(dev, "moe_route_topk", lib.moe_route_topk, logits.data_ptr(), code, _ptr(bias), score, T, E, topk, n_group,
+            topk_group, group_top, int(renormalise), scale, out[0].data_ptr(), out[1].data_ptr())
+    return out
+
+
+def moe_workspace_bytes(T, topk, I):
+    """Bytes of workspace moe_w8a8_block needs."""
+    n = lib.moe_workspace_bytes(T, topk, I)
+    _check(min(n, 0), "moe_workspace_bytes")
+    return n
+
+
+def moe_w8a8_block(A, a_scale, topk_ids, topk_weights, W_gate_up, gate_up_scale, W_down, down_scale,
+                   out_dtype=torch.bfloat16, out=None, workspace=None):
+    """A whole mixture-of-experts layer for up to 64 tokens (block-wise scheme):
+    Y[t] = sum_j topk_weights[t, j] * down_e(quant(silu(gate_e) * up_e)), e = topk_ids[t, j].
+
+    A int8 [T, K] with a_scale [T, K/128] (quant_act_group or
+    norm_residual_quant); topk_ids int32 and topk_weights fp32 [T, topk] (ids
+    outside 0 .. E-1 add nothing); W_gate_up int8 [E, 2I, K] (gate rows first)
+    with gate_up_scale [E, 2I/128, K/128]; W_down int8 [E, K, I] with
+    down_scale [E, K/128, I/128].  workspace: uint8, moe_workspace_bytes(T,
+    topk, I) or more; without one, torch allocates it for the call.
+    """
+    _dev(A)
+    T, K = A.shape
+    E, I2, _ = W_gate_up.shape
+    topk, I, dev = topk_ids.shape[1], I2 // 2, A.device
+    _like(A, "A", (T, K), torch.int8, dev)
+    _like(a_scale, "a_scale", (T, K // GROUP), torch.float32, dev)
+    _like(topk_ids, "topk_ids", (T, topk), torch.int32, dev)
+    _like(topk_weights, "topk_weights", (T, topk), torch.float32, dev)
+    _like(W_gate_up, "W_gate_up", (E, 2 * I, K), torch.int8, dev)
+    _like(gate_up_scale, "gate_up_scale", (E, 2 * I // GROUP, K // GROUP), torch.float32, dev)
+    _like(W_down, "W_down", (E, K, I), torch.int8, dev)
+    _like(down_scale, "down_scale", (E, K // GROUP, I // GROUP), torch.float32, dev)
+    if out is None:
+        out = torch.empty((T, K), dtype=out_dtype, device=dev)
+    else:
+        _like(out, "out", (T, K), out.dtype, dev)
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise W8Error(f"moe_w8a8_block writes bf16 or fp32, not {out.dtype}")
+    if workspace is None:
+        workspace = torch.empty((moe_workspace_bytes(T, topk, I),), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise W8Error(f"workspace must be contiguous, on {dev}")
+    _run_on(dev, "moe_w8a8_block", lib.moe_w8a8_block, A.data_ptr(), a_scale.data_ptr(), topk_ids.data_ptr(),
+            topk_weights.data_ptr(), W_gate_up.data_ptr(), gate_up_scale.data_ptr(), W_down.data_ptr(),
+            down_scale.data_ptr(), out.data_ptr(), _out_code(out.dtype), T, topk, E, I, K, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+    return out

@@ -81,6 +81,7 @@ const char* w8_status_string(int status) {
     case W8_ERR_CAPTURE:
       return "the call would allocate its scratch while its stream is being captured "
              "(make one call of the largest shape on the stream before capturing)";
+    case W8_ERR_VALUE: return "argument value out of range";
     default: return "unknown status";
   }
 }
@@ -352,6 +353,127 @@ int gemm_w8a8_asym(const int8_t* A_shifted, const float* a_params, const int8_t*
   if (!aligned(a_params, 4) || !aligned(w_scale, 4) || !aligned(w_sum, 4)) return W8_ERR_ALIGN;
   return status_of(
       w8::launch_gemm_asym(A_shifted, a_params, W, w_scale, w_sum, Y, out, M, N, K, as_stream(stream)));
+}
+
+int norm_residual_quant(const void* y, const void* residual, const void* post_weight, const void* gate,
+                        int64_t gate_rows, float residual_scale, const void* pre_weight, float eps, int dtype,
+                        int scheme, int64_t M, int64_t K, void* h, void* normed, int8_t* q, float* q_scale,
+                        void* stream) {
+  if (dtype != W8_BF16 && dtype != W8_FP16) return W8_ERR_DTYPE;
+  if (scheme != W8_SCHEME_BLOCK && scheme != W8_SCHEME_CHANNEL) return W8_ERR_DTYPE;
+  int rc = check_rows_k(M, K);
+  if (rc) return rc;
+  if (K > w8::kNormMaxK || (gate && gate_rows != 1 && gate_rows != M)) return W8_ERR_SHAPE;
+  // written so that a NaN fails
+  if (!(eps > 0.f && eps <= 3.4e38f) || !(residual_scale >= -3.4e38f && residual_scale <= 3.4e38f))
+    return W8_ERR_VALUE;
+  if (M == 0) return W8_OK;
+  if (K == 0) return W8_ERR_SHAPE;
+  if (!y || !pre_weight || !h || !(normed || q) || (q && !q_scale)) return W8_ERR_NULL;
+  for (const void* p : {y, residual, post_weight, gate, pre_weight, static_cast<const void*>(h),
+                        static_cast<const void*>(normed), static_cast<const void*>(q)})
+    if (!aligned(p, 16)) return W8_ERR_ALIGN;
+  if (!aligned(q_scale, 4)) return W8_ERR_ALIGN;
+  w8::NormArgs a;
+  a.y = y;
+  a.residual = residual;
+  a.post_weight = post_weight;
+  a.gate = gate;
+  a.pre_weight = pre_weight;
+  a.h = h;
+  a.z = normed;
+  a.q = q;
+  a.q_scale = q_scale;
+  a.gate_rows = gate_rows;
+  a.K = (int)K;
+  a.residual_scale = residual_scale;
+  a.eps = eps;
+  a.group = scheme == W8_SCHEME_BLOCK;
+  return status_of(w8::launch_norm_residual_quant(a, dtype == W8_FP16, M, as_stream(stream)));
+}
+
+int moe_route_topk(const void* logits, int logits_dtype, const float* bias, int score, int64_t T, int64_t E,
+                   int topk, int n_group, int topk_group, int group_top, int renormalise, double scale, int32_t* ids,
+                   float* weights, void* stream) {
+  if (logits_dtype != W8_BF16 && logits_dtype != W8_FP16 && logits_dtype != W8_FP32) return W8_ERR_DTYPE;
+  if (score != W8_ROUTE_SOFTMAX && score != W8_ROUTE_SIGMOID) return W8_ERR_DTYPE;
+  if (T < 0 || T > kMaxRows || E < 1 || E > w8::kRouteMaxE || topk < 1 || topk > w8::kRouteMaxTopk)
+    return W8_ERR_SHAPE;
+  if (n_group < 1 || E % n_group != 0 || topk_group < 1 || topk_group > n_group) return W8_ERR_SHAPE;
+  if (topk > topk_group * (E / n_group)) return W8_ERR_SHAPE;
+  if (group_top != 1 && group_top != 2) return W8_ERR_VALUE;
+  if (!(scale >= -3.4e38 && scale <= 3.4e38)) return W8_ERR_VALUE;
+  if (T == 0) return W8_OK;
+  if (!logits || !ids || !weights) return W8_ERR_NULL;
+  if (!aligned(logits, logits_dtype == W8_FP32 ? 4 : 2) || !aligned(bias, 4) || !aligned(ids, 4) ||
+      !aligned(weights, 4))
+    return W8_ERR_ALIGN;
+  w8::RouteArgs a;
+  a.logits = logits;
+  a.bias = bias;
+  a.ids = ids;
+  a.weights = weights;
+  a.scale = scale;
+  a.E = (int)E;
+  a.topk = topk;
+  a.n_group = n_group;
+  a.topk_group = topk_group;
+  a.group_top = group_top;
+  a.dtype = logits_dtype;
+  a.sigmoid = score == W8_ROUTE_SIGMOID;
+  a.renormalise = renormalise != 0;
+  return status_of(w8::launch_route_topk(a, T, as_stream(stream)));
+}
+
+// The size rules of the few-token layer, shared by the call and its workspace query.
+static int check_moe(int64_t T, int64_t topk, int64_t I) {
+  if (T < 0 || T > w8::kMoeMaxT || topk < 1 || topk > w8::kMoeMaxTopk) return W8_ERR_SHAPE;
+  if (I < 128 || I > w8::kMoeMaxSide || (I & 127) != 0) return W8_ERR_SHAPE;
+  return W8_OK;
+}
+
+int64_t moe_workspace_bytes(int64_t T, int64_t topk, int64_t I) {
+  int rc = check_moe(T, topk, I);
+  return rc ? rc : w8::moe_workspace(T, topk, I, nullptr, nullptr);
+}
+
+int moe_w8a8_block(const int8_t* A, const float* a_scale, const int32_t* topk_ids, const float* topk_weights,
+                   const int8_t* W_gate_up, const float* gate_up_scale, const int8_t* W_down,
+                   const float* down_scale, void* Y, int y_dtype, int64_t T, int64_t topk, int64_t E, int64_t I,
+                   int64_t K, void* workspace, int64_t workspace_bytes, void* stream) {
+  w8::OutKind out;
+  int rc = check_out(y_dtype, false, &out);
+  if (rc) return rc;
+  rc = check_moe(T, topk, I);
+  if (rc) return rc;
+  if (E < 1 || E > w8::kMoeMaxE || K < 128 || K > w8::kMoeMaxSide || (K & 127) != 0) return W8_ERR_SHAPE;
+  if (2 * I * K > kMaxElems / E) return W8_ERR_SHAPE;
+  if (T == 0) return W8_OK;
+  if (!A || !a_scale || !topk_ids || !topk_weights || !W_gate_up || !gate_up_scale || !W_down || !down_scale || !Y ||
+      !workspace)
+    return W8_ERR_NULL;
+  if (!aligned(A, 16) || !aligned(W_gate_up, 16) || !aligned(W_down, 16) || !aligned(Y, 16) ||
+      !aligned(workspace, 256) || !aligned(a_scale, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) ||
+      !aligned(gate_up_scale, 4) || !aligned(down_scale, 4))
+    return W8_ERR_ALIGN;
+  if (workspace_bytes < w8::moe_workspace(T, topk, I, nullptr, nullptr)) return W8_ERR_WORKSPACE;
+  w8::MoeArgs a;
+  a.A = A;
+  a.sa = a_scale;
+  a.ids = topk_ids;
+  a.weights = topk_weights;
+  a.w13 = W_gate_up;
+  a.s13 = gate_up_scale;
+  a.w2 = W_down;
+  a.s2 = down_scale;
+  a.Y = Y;
+  a.T = (int)T;
+  a.topk = (int)topk;
+  a.E = (int)E;
+  a.I = (int)I;
+  a.K = (int)K;
+  w8::moe_workspace(T, topk, I, &a, workspace);
+  return status_of(w8::launch_moe_block(a, out, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -65,6 +65,56 @@ hipError_t launch_gemm_w4a16(const uint16_t* x, const uint8_t* W4, const float* 
 hipError_t launch_quant_weight_int4(const void* w, bool fp16, int64_t N, int64_t K, uint8_t* q4, float* s,
                                     hipStream_t st);
 
+// The norms between two blocks with the quantiser behind them (norm.hip);
+// pointers that may be null: residual, post_weight, gate, z, q (with q_scale).
+struct NormArgs {
+  const void *y, *residual, *post_weight, *gate, *pre_weight;
+  void *h, *z;
+  int8_t* q;
+  float* q_scale;
+  int64_t gate_rows;   // 1 or M
+  int K;
+  float residual_scale, eps;
+  bool group;          // the quantiser's granularity: 1 x 128, or a row
+};
+hipError_t launch_norm_residual_quant(const NormArgs& a, bool fp16, int64_t M, hipStream_t st);
+constexpr int64_t kNormMaxK = 32768;
+
+// The router of a mixture-of-experts layer (route.hip).
+struct RouteArgs {
+  const void* logits;
+  const float* bias;
+  int32_t* ids;
+  float* weights;
+  double scale;
+  int E, topk, n_group, topk_group, group_top, dtype;   // dtype: a w8_dtype
+  bool sigmoid, renormalise;
+};
+hipError_t launch_route_topk(const RouteArgs& a, int64_t T, hipStream_t st);
+constexpr int64_t kRouteMaxE = 1024, kRouteMaxTopk = 64;
+
+// A mixture-of-experts layer for a few tokens (moe.hip).  hq .. start lie in
+// the caller's workspace: moe_workspace gives its size and, with a and ws,
+// sets them.
+struct MoeArgs {
+  const int8_t* A;
+  const float* sa;
+  const int32_t* ids;
+  const float* weights;
+  const int8_t* w13;
+  const float* s13;
+  const int8_t* w2;
+  const float* s2;
+  void* Y;
+  int8_t* hq;
+  float* hs;
+  int32_t *pos, *count, *start;
+  int T, topk, E, I, K;
+};
+int64_t moe_workspace(int64_t T, int64_t topk, int64_t I, MoeArgs* a, void* ws);
+hipError_t launch_moe_block(const MoeArgs& a, OutKind out, hipStream_t st);
+constexpr int64_t kMoeMaxT = 64, kMoeMaxTopk = 16, kMoeMaxSide = 1 << 17, kMoeMaxE = 4096;
+
 // The library's own scratch (rules in workspace.h): at least `bytes` of
 // device memory for (current device, `st`, `slot`), slot 0 for split-K
 // partial tiles, slot 1 for the asymmetric path.  The lease holds the

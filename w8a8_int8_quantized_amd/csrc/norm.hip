@@ -1,0 +1,201 @@
+// The norms between two blocks, the residual between them and the quantiser
+// behind them, in one pass over the row (gfx950).
+//
+//   n = y * rsqrt(mean(y^2) + eps) * post_weight       (n = y without one)
+//   h = t(residual + residual_scale * (gate * n))      t: the 16-bit type
+//   z = t(h * rsqrt(mean(h^2) + eps) * pre_weight)
+//   q, s = the symmetric INT8 quantiser of z, per 1 x 128 group or per row
+//
+// Quantiser: the page "FP8 vs INT8 quantisation for DeepSeek", section 3.2.1
+// (int8 branch), at the granularities of "DeepSeek R1 INT8 quantisation in
+// SGLang", section 2.3.  The second norm reads h as it is stored (rounded to
+// t) and the quantiser reads z rounded to t, so a layer that takes 16-bit
+// inputs and one that takes the codes see the same activations, and the codes
+// are those of quant_act_group / quant_act_token on z, bit for bit.  All else
+// is fp32: squares, their sums, products.
+#include "common.h"
+#include "launch.h"
+
+namespace w8 {
+namespace {
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+
+// Sum or maximum over a workgroup of NW waves; every thread gets it.  red
+// holds NW floats that nothing else uses between this call's barrier and the
+// next call on the same array.
+template <int NW>
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  v = wave_sum(v);
+  if (NW == 1) return v;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float r = red[0];
+#pragma unroll
+  for (int w = 1; w < NW; ++w) r += red[w];
+  return r;
+}
+
+template <int NW>
+__device__ __forceinline__ float block_max(float v, float* red) {
+  v = wave_max(v);
+  if (NW == 1) return v;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float r = red[0];
+#pragma unroll
+  for (int w = 1; w < NW; ++w) r = fmaxf(r, red[w]);
+  return r;
+}
+
+// 8 fp32 values to the 16-bit type (round to nearest even), packed.
+template <bool FP16>
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (FP16) {
+      const uint16_t a = __builtin_bit_cast(uint16_t, (_Float16)v[2 * i]);
+      const uint16_t b = __builtin_bit_cast(uint16_t, (_Float16)v[2 * i + 1]);
+      w[i] = (uint32_t)a | ((uint32_t)b << 16);
+    } else {
+      w[i] = f32_to_bf16_rne(v[2 * i]) | (f32_to_bf16_rne(v[2 * i + 1]) << 16);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One workgroup of NT threads per row; thread t holds the 8-value chunks t,
+// t + NT, ... (CH of them at most), so the row is read once and stays in
+// registers through both norms and the quantiser.  A 128-value group is the
+// 16 chunks of 16 neighbouring lanes.
+template <bool FP16, int NT, int CH>
+__global__ __launch_bounds__(NT) void k_norm_residual_quant(NormArgs a) {
+  constexpr int NW = NT / 64;
+  __shared__ float red[3][NW];
+  const int64_t row = blockIdx.x;
+  const int nch = a.K >> 3;
+  const uint4* y = static_cast<const uint4*>(a.y) + row * nch;
+  const uint4* res = a.residual ? static_cast<const uint4*>(a.residual) + row * nch : nullptr;
+  const uint4* gate = a.gate ? static_cast<const uint4*>(a.gate) + (a.gate_rows == 1 ? 0 : row * nch) : nullptr;
+  const uint4* pw = static_cast<const uint4*>(a.post_weight);
+  const uint4* nw = static_cast<const uint4*>(a.pre_weight);
+  const float inv_k = 1.0f / (float)a.K;
+
+  uint4 raw[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = threadIdx.x + NT * i;
+    if (c < nch) raw[i] = y[c];
+  }
+  float inv = 1.0f;
+  if (pw) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      if (threadIdx.x + NT * i < nch) {
+        float v[8];
+        unpack8<FP16>(raw[i], v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
+      }
+    }
+    inv = 1.0f / __builtin_sqrtf(block_sum<NW>(ss, red[0]) * inv_k + a.eps);
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = threadIdx.x + NT * i;
+    if (c < nch) {
+      float v[8], o[8];
+      unpack8<FP16>(raw[i], v);
+      if (pw) {
+        unpack8<FP16>(pw[c], o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = v[e] * inv * o[e];
+      }
+      if (gate) {
+        unpack8<FP16>(gate[c], o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= o[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= a.residual_scale;
+      if (res) {
+        unpack8<FP16>(res[c], o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += o[e];
+      }
+      raw[i] = pack8<FP16>(v);
+      static_cast<uint4*>(a.h)[row * nch + c] = raw[i];
+      unpack8<FP16>(raw[i], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
+    }
+  }
+  inv = 1.0f / __builtin_sqrtf(block_sum<NW>(ss, red[1]) * inv_k + a.eps);
+
+  float am[CH];
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = threadIdx.x + NT * i;
+    am[i] = 0.f;
+    if (c < nch) {
+      float v[8], o[8];
+      unpack8<FP16>(raw[i], v);
+      unpack8<FP16>(nw[c], o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = v[e] * inv * o[e];
+      raw[i] = pack8<FP16>(v);
+      if (a.z) static_cast<uint4*>(a.z)[row * nch + c] = raw[i];
+      unpack8<FP16>(raw[i], v);
+      am[i] = amax_n(v, 8);
+      amax = fmaxf(amax, am[i]);
+    }
+  }
+  if (!a.q) return;
+  const bool group = a.group;
+  if (!group) amax = block_max<NW>(amax, red[2]);
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = threadIdx.x + NT * i;
+    // a group's 16 lanes are all inside the row or all outside it
+    const QScale sc = make_scale(group ? max16(am[i]) : amax);
+    if (c < nch) {
+      float v[8];
+      unpack8<FP16>(raw[i], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = quant_one(v[e], sc);
+      uint2 o;
+      o.x = pack4(v[0], v[1], v[2], v[3]);
+      o.y = pack4(v[4], v[5], v[6], v[7]);
+      reinterpret_cast<uint2*>(a.q + row * (int64_t)a.K)[c] = o;
+      if (group && (c & 15) == 0) a.q_scale[row * (a.K >> 7) + (c >> 4)] = sc.s;
+    }
+  }
+  if (!group && threadIdx.x == 0) a.q_scale[row] = make_scale(amax).s;
+}
+
+template <bool FP16>
+hipError_t norm_launch(const NormArgs& a, int64_t M, hipStream_t st) {
+  const dim3 grid((unsigned)M);
+  const int nch = a.K >> 3;
+  if (nch <= 1024)
+    hipLaunchKernelGGL((k_norm_residual_quant<FP16, 256, 4>), grid, dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_norm_residual_quant<FP16, 1024, 4>), grid, dim3(1024), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_norm_residual_quant(const NormArgs& a, bool fp16, int64_t M, hipStream_t st) {
+  return fp16 ? norm_launch<true>(a, M, st) : norm_launch<false>(a, M, st);
+}
+
+}  // namespace w8
