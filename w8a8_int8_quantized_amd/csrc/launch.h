@@ -93,7 +93,7 @@ struct RouteArgs {
 hipError_t launch_route_topk(const RouteArgs& a, int64_t T, hipStream_t st);
 constexpr int64_t kRouteMaxE = 1024, kRouteMaxTopk = 64;
 
-// A mixture-of-experts layer for a few tokens (moe.hip).  hq .. start lie in
+// A mixture-of-experts layer for a few tokens (moe.hip).  h32 .. start lie in
 // the caller's workspace: moe_workspace gives its size and, with a and ws,
 // sets them.
 struct MoeArgs {
@@ -106,9 +106,10 @@ struct MoeArgs {
   const int8_t* w2;
   const float* s2;
   void* Y;
+  float* h32;
   int8_t* hq;
   float* hs;
-  int32_t *pos, *count, *start;
+  int32_t *pos, *expert, *count, *start;
   int T, topk, E, I, K;
 };
 int64_t moe_workspace(int64_t T, int64_t topk, int64_t I, MoeArgs* a, void* ws);
