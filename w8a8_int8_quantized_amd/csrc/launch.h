@@ -89,8 +89,9 @@ struct RouteArgs {
   double scale;
   int E, topk, n_group, topk_group, group_top, dtype;   // dtype: a w8_dtype
   bool sigmoid, renormalise;
+  uint32_t per_magic;   // set by the launcher: e / (E / n_group) = e * per_magic >> 20
 };
-hipError_t launch_route_topk(const RouteArgs& a, int64_t T, hipStream_t st);
+hipError_t launch_route_topk(RouteArgs a, int64_t T, hipStream_t st);
 constexpr int64_t kRouteMaxE = 1024, kRouteMaxTopk = 64;
 
 // A mixture-of-experts layer for a few tokens (moe.hip).  h32 .. start lie in

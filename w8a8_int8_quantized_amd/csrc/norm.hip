@@ -19,6 +19,9 @@
 namespace w8 {
 namespace {
 
+// Up to this many rows a row is spread over 1024 threads, one chunk each.
+constexpr int64_t kNormFewRows = 256;
+
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
@@ -69,6 +72,23 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// One row of a 16-bit array (or an empty range where the array is absent) as
+// a buffer: a load past its end, or of an absent array, reads zeros and moves
+// nothing, so no load sits under a branch and all of a row's loads are under
+// way before the first is waited for.
+struct Row {
+  __amdgpu_buffer_rsrc_t r;
+  __device__ __forceinline__ Row(const void* base, int64_t row, int K) {
+    const uint64_t at = (uint64_t)base + (uint64_t)row * (uint64_t)K * 2;
+    const uint64_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)at);
+    const uint64_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(at >> 32));
+    r = __builtin_amdgcn_make_buffer_rsrc((void*)(lo | (hi << 32)), 0, base ? K * 2 : 0, 0x00020000);
+  }
+  __device__ __forceinline__ uint4 chunk(int c) const {
+    return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, c * 16, 0, 0));
+  }
+};
+
 // One workgroup of NT threads per row; thread t holds the 8-value chunks t,
 // t + NT, ... (CH of them at most), so the row is read once and stays in
 // registers through both norms and the quantiser.  A 128-value group is the
@@ -79,30 +99,30 @@ __global__ __launch_bounds__(NT) void k_norm_residual_quant(NormArgs a) {
   __shared__ float red[3][NW];
   const int64_t row = blockIdx.x;
   const int nch = a.K >> 3;
-  const uint4* y = static_cast<const uint4*>(a.y) + row * nch;
-  const uint4* res = a.residual ? static_cast<const uint4*>(a.residual) + row * nch : nullptr;
-  const uint4* gate = a.gate ? static_cast<const uint4*>(a.gate) + (a.gate_rows == 1 ? 0 : row * nch) : nullptr;
-  const uint4* pw = static_cast<const uint4*>(a.post_weight);
-  const uint4* nw = static_cast<const uint4*>(a.pre_weight);
+  const Row y(a.y, row, a.K), res(a.residual, row, a.K), gate(a.gate, a.gate_rows == 1 ? 0 : row, a.K),
+      pw(a.post_weight, 0, a.K), nw(a.pre_weight, 0, a.K);
   const float inv_k = 1.0f / (float)a.K;
 
-  uint4 raw[CH];
+  uint4 raw[CH], rr[CH], rg[CH], rp[CH], rn[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) raw[i] = y.chunk(threadIdx.x + NT * i);
+#pragma unroll
+  for (int i = 0; i < CH; ++i) rr[i] = res.chunk(threadIdx.x + NT * i);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int c = threadIdx.x + NT * i;
-    if (c < nch) raw[i] = y[c];
+    rg[i] = gate.chunk(threadIdx.x + NT * i);
+    rp[i] = pw.chunk(threadIdx.x + NT * i);
+    rn[i] = nw.chunk(threadIdx.x + NT * i);
   }
   float inv = 1.0f;
-  if (pw) {
+  if (a.post_weight) {
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      if (threadIdx.x + NT * i < nch) {
-        float v[8];
-        unpack8<FP16>(raw[i], v);
+      float v[8];
+      unpack8<FP16>(raw[i], v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
-      }
+      for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
     }
     inv = 1.0f / __builtin_sqrtf(block_sum<NW>(ss, red[0]) * inv_k + a.eps);
   }
@@ -110,32 +130,26 @@ __global__ __launch_bounds__(NT) void k_norm_residual_quant(NormArgs a) {
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = threadIdx.x + NT * i;
-    if (c < nch) {
-      float v[8], o[8];
-      unpack8<FP16>(raw[i], v);
-      if (pw) {
-        unpack8<FP16>(pw[c], o);
+    float v[8], o[8];
+    unpack8<FP16>(raw[i], v);
+    if (a.post_weight) {
+      unpack8<FP16>(rp[i], o);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = v[e] * inv * o[e];
-      }
-      if (gate) {
-        unpack8<FP16>(gate[c], o);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= o[e];
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= a.residual_scale;
-      if (res) {
-        unpack8<FP16>(res[c], o);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += o[e];
-      }
-      raw[i] = pack8<FP16>(v);
-      static_cast<uint4*>(a.h)[row * nch + c] = raw[i];
-      unpack8<FP16>(raw[i], v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
+      for (int e = 0; e < 8; ++e) v[e] = v[e] * inv * o[e];
     }
+    if (a.gate) {
+      unpack8<FP16>(rg[i], o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= o[e];
+    }
+    unpack8<FP16>(rr[i], o);   // zeros without a residual
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = v[e] * a.residual_scale + o[e];
+    raw[i] = pack8<FP16>(v);
+    if (c < nch) static_cast<uint4*>(a.h)[row * nch + c] = raw[i];
+    unpack8<FP16>(raw[i], v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
   }
   inv = 1.0f / __builtin_sqrtf(block_sum<NW>(ss, red[1]) * inv_k + a.eps);
 
@@ -144,19 +158,16 @@ __global__ __launch_bounds__(NT) void k_norm_residual_quant(NormArgs a) {
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = threadIdx.x + NT * i;
-    am[i] = 0.f;
-    if (c < nch) {
-      float v[8], o[8];
-      unpack8<FP16>(raw[i], v);
-      unpack8<FP16>(nw[c], o);
+    float v[8], o[8];
+    unpack8<FP16>(raw[i], v);
+    unpack8<FP16>(rn[i], o);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = v[e] * inv * o[e];
-      raw[i] = pack8<FP16>(v);
-      if (a.z) static_cast<uint4*>(a.z)[row * nch + c] = raw[i];
-      unpack8<FP16>(raw[i], v);
-      am[i] = amax_n(v, 8);
-      amax = fmaxf(amax, am[i]);
-    }
+    for (int e = 0; e < 8; ++e) v[e] = v[e] * inv * o[e];
+    raw[i] = pack8<FP16>(v);
+    if (a.z && c < nch) static_cast<uint4*>(a.z)[row * nch + c] = raw[i];
+    unpack8<FP16>(raw[i], v);
+    am[i] = amax_n(v, 8);
+    amax = fmaxf(amax, am[i]);
   }
   if (!a.q) return;
   const bool group = a.group;
@@ -166,11 +177,11 @@ __global__ __launch_bounds__(NT) void k_norm_residual_quant(NormArgs a) {
     const int c = threadIdx.x + NT * i;
     // a group's 16 lanes are all inside the row or all outside it
     const QScale sc = make_scale(group ? max16(am[i]) : amax);
-    if (c < nch) {
-      float v[8];
-      unpack8<FP16>(raw[i], v);
+    float v[8];
+    unpack8<FP16>(raw[i], v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = quant_one(v[e], sc);
+    for (int e = 0; e < 8; ++e) v[e] = quant_one(v[e], sc);
+    if (c < nch) {
       uint2 o;
       o.x = pack4(v[0], v[1], v[2], v[3]);
       o.y = pack4(v[4], v[5], v[6], v[7]);
@@ -181,15 +192,20 @@ __global__ __launch_bounds__(NT) void k_norm_residual_quant(NormArgs a) {
   if (!group && threadIdx.x == 0) a.q_scale[row] = make_scale(amax).s;
 }
 
+template <bool FP16, int NT, int CH>
+hipError_t norm_go(const NormArgs& a, int64_t M, hipStream_t st) {
+  hipLaunchKernelGGL((k_norm_residual_quant<FP16, NT, CH>), dim3((unsigned)M), dim3(NT), 0, st, a);
+  return hipGetLastError();
+}
+
 template <bool FP16>
 hipError_t norm_launch(const NormArgs& a, int64_t M, hipStream_t st) {
-  const dim3 grid((unsigned)M);
   const int nch = a.K >> 3;
-  if (nch <= 1024)
-    hipLaunchKernelGGL((k_norm_residual_quant<FP16, 256, 4>), grid, dim3(256), 0, st, a);
-  else
-    hipLaunchKernelGGL((k_norm_residual_quant<FP16, 1024, 4>), grid, dim3(1024), 0, st, a);
-  return hipGetLastError();
+  if (nch > 1024) return norm_go<FP16, 1024, 4>(a, M, st);
+  if (M <= kNormFewRows) return nch <= 256 ? norm_go<FP16, 256, 1>(a, M, st) : norm_go<FP16, 1024, 1>(a, M, st);
+  if (nch <= 256) return norm_go<FP16, 256, 1>(a, M, st);
+  if (nch <= 512) return norm_go<FP16, 256, 2>(a, M, st);
+  return norm_go<FP16, 256, 4>(a, M, st);
 }
 
 }  // namespace

@@ -10,123 +10,218 @@
 // Scores and choice are computed in 64 bits: the choice is a comparison of
 // numbers that may lie anywhere near each other, and in 32 bits the rounding
 // of exp and of the sum would decide between experts whose logits differ.
+//
+// One wave per token, no barriers: expert i 64 + lane is element i of a lane,
+// so everything up to the choice is in registers.  The choice takes the
+// largest c topk times.  c is held as an unsigned integer of the same order,
+// split into two words: the largest high word is found with four DPP steps
+// and four scalar maxima, and only experts that tie in it are compared in the
+// low word (a workgroup per token with a count of the better experts for each
+// took 10.8 us for one token of 256 experts and 52 us for 4096).
 #include "common.h"
 #include "launch.h"
 
 namespace w8 {
 namespace {
 
-__device__ __forceinline__ double block_reduce(double v, bool mx, double* red, int nw) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    const double o = __shfl_xor(v, d, 64);
-    v = mx ? fmax(v, o) : v + o;
-  }
-  if (nw > 1) {
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = red[0];
-    for (int w = 1; w < nw; ++w) v = mx ? fmax(v, red[w]) : v + red[w];
-  }
-  return v;
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+  v = umax(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));    // quad_perm [1,0,3,2]
+  v = umax(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));    // quad_perm [2,3,0,1]
+  v = umax(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));   // row_half_mirror
+  v = umax(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, false));   // row_ror:8
+  return umax(umax((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 16)),
+              umax((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48)));
 }
 
-// One workgroup per token, one expert per thread (blockDim.x >= E).  An
-// expert's place in the order is the number of experts before it: larger c,
-// or equal c and a lower index.  Places are distinct whatever the values
-// (masked experts hold -inf), so each of the topk slots is written once.
-__global__ __launch_bounds__(1024) void k_route_topk(RouteArgs a) {
-  __shared__ double c[1024];
-  __shared__ double top[1024][2];
-  __shared__ double sel[64];
-  __shared__ double red[2][16];
-  __shared__ uint8_t stays[1024];
+__device__ __forceinline__ double lane_double(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint64_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+  const uint64_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+  return __builtin_bit_cast(double, lo | (hi << 32));
+}
+
+// NE: elements per lane (E <= 64 NE).  Dynamic LDS: c [E] and s [E], then
+// (n_group > 1) the groups' scores [n_group] and a byte each.
+template <int NE>
+__global__ __launch_bounds__(64) void k_route_topk(RouteArgs a) {
+  extern __shared__ double lds[];
+  const int E = a.E, lane = threadIdx.x;
   const int64_t t = blockIdx.x;
-  const int e = threadIdx.x;
-  const int E = a.E, nw = blockDim.x >> 6;
-  const bool in = e < E;
+  double* lc = lds;
+  double* lw = lc + E;
+  double* gs = lw + E;
+  uint8_t* stays = reinterpret_cast<uint8_t*>(gs + a.n_group);
   const double ninf = -__builtin_inf();
-  float lf = -__builtin_inff();
-  if (in) {
-    const int64_t i = t * E + e;
-    if (a.dtype == 2) {
-      lf = static_cast<const float*>(a.logits)[i];
-    } else {
-      const uint32_t b = static_cast<const uint16_t*>(a.logits)[i];
-      lf = a.dtype == 1 ? h2f(b) : bf16_lo(b);
+
+  float lf[NE], bias[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const int e = i * 64 + lane;
+    lf[i] = -__builtin_inff();
+    bias[i] = 0.f;
+    if (e < E) {
+      if (a.dtype == 2) {
+        lf[i] = static_cast<const float*>(a.logits)[t * E + e];
+      } else {
+        const uint32_t b = static_cast<const uint16_t*>(a.logits)[t * E + e];
+        lf[i] = a.dtype == 1 ? h2f(b) : bf16_lo(b);
+      }
+      if (a.bias) bias[i] = a.bias[e];
     }
   }
-  // a NaN compares false: masked, as -inf is; +inf is the largest finite
-  const bool live = lf > -__builtin_inff();
-  const double l = live ? (double)fminf(lf, 3.40282347e38f) : ninf;
-  double s;
-  if (a.sigmoid) {
-    s = live ? 1.0 / (1.0 + exp(-l)) : 0.0;
-  } else {
-    const double mx = block_reduce(l, true, red[0], nw);
-    s = live ? exp(l - mx) : 0.0;
-    const double sum = block_reduce(s, false, red[1], nw);
-    s = sum > 0.0 ? s / sum : 0.0;
+  double s[NE];
+  bool live[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    // a NaN compares false: masked, as -inf is; +inf is the largest finite
+    live[i] = lf[i] > -__builtin_inff();
+    lf[i] = live[i] ? fminf(lf[i], 3.40282347e38f) : -__builtin_inff();
   }
-  double ce = live ? (a.bias ? s + (double)a.bias[e] : s) : ninf;
-  if (!(ce > ninf)) ce = ninf;   // a NaN bias masks its expert too
-  if (in) c[e] = ce;
-  __syncthreads();
+  if (a.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) s[i] = live[i] ? 1.0 / (1.0 + exp(-(double)lf[i])) : 0.0;
+  } else {
+    float mx = lf[0];
+#pragma unroll
+    for (int i = 1; i < NE; ++i) mx = fmaxf(mx, lf[i]);
+    mx = wave_max(mx);
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      s[i] = live[i] ? exp((double)lf[i] - (double)mx) : 0.0;
+      sum += s[i];
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, 64);
+#pragma unroll
+    for (int i = 0; i < NE; ++i) s[i] = sum > 0.0 ? s[i] / sum : 0.0;
+  }
+  double c[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const int e = i * 64 + lane;
+    c[i] = live[i] ? (a.bias ? s[i] + (double)bias[i] : s[i]) : ninf;
+    if (!(c[i] > ninf)) c[i] = ninf;   // a NaN bias masks its expert too
+    if (e < E) {
+      lc[e] = c[i];
+      lw[e] = s[i];
+    }
+  }
+  __syncthreads();   // one wave: orders its LDS accesses only
   if (a.n_group > 1) {
     const int per = E / a.n_group;
-    const int g = in ? e / per : 0;
-    if (in) {
+    // w lanes to a group take every w-th of its experts, then join
+    int w = 1;
+    while (w * 2 * a.n_group <= 64) w *= 2;
+    for (int g0 = 0; g0 < a.n_group; g0 += 64 / w) {
+      const int g = g0 + lane / w;
+      double b1 = ninf, b2 = ninf;
+      if (g < a.n_group)
+        for (int j = lane & (w - 1); j < per; j += w) {
+          const double v = lc[g * per + j];
+          if (v > b1) {
+            b2 = b1;
+            b1 = v;
+          } else if (v > b2) {
+            b2 = v;
+          }
+        }
+      for (int d = 1; d < w; d <<= 1) {
+        const double o1 = __shfl_xor(b1, d, 64), o2 = __shfl_xor(b2, d, 64);
+        const double low = o1 < b1 ? o1 : b1, second = o2 > b2 ? o2 : b2;
+        b1 = o1 > b1 ? o1 : b1;
+        b2 = low > second ? low : second;
+      }
+      if (g < a.n_group && (lane & (w - 1)) == 0) gs[g] = a.group_top == 2 && b2 > ninf ? b1 + b2 : b1;
+    }
+    __syncthreads();
+    for (int g = lane; g < a.n_group; g += 64) {
+      const double v = gs[g];
       int place = 0;
-      for (int j = g * per; j < g * per + per; ++j) place += c[j] > ce || (c[j] == ce && j < e);
-      if (place < 2) top[g][place] = ce;
+      for (int j = 0; j < a.n_group; ++j) place += gs[j] > v || (gs[j] == v && j < g);
+      stays[g] = place < a.topk_group;
     }
     __syncthreads();
-    double* gs = &top[0][0];
-    double score = 0.0;
-    if (e < a.n_group) {
-      score = top[e][0];
-      if (a.group_top == 2 && per > 1 && top[e][1] > ninf) score += top[e][1];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      const int e = i * 64 + lane;
+      // e / per: exact for e < 1024 and per < 1024
+      if (e < E && !stays[((uint32_t)e * a.per_magic) >> 20]) c[i] = ninf;
     }
-    __syncthreads();
-    if (e < a.n_group) gs[e] = score;
-    __syncthreads();
-    if (e < a.n_group) {
-      int place = 0;
-      for (int j = 0; j < a.n_group; ++j) place += gs[j] > score || (gs[j] == score && j < e);
-      stays[e] = place < a.topk_group;
+  }
+
+  // the same order as unsigned integers, 0 for an expert that cannot be chosen
+  uint32_t hi[NE], lo[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    uint64_t b = __builtin_bit_cast(uint64_t, c[i] + 0.0);   // -0 becomes 0
+    b = b >> 63 ? ~b : b | (1ull << 63);
+    if (!(c[i] > ninf)) b = 0;
+    hi[i] = (uint32_t)(b >> 32);
+    lo[i] = (uint32_t)b;
+  }
+  int mine = -1;   // lane j: the j-th choice
+  for (int j = 0; j < a.topk; ++j) {
+    uint32_t v = hi[0];
+#pragma unroll
+    for (int i = 1; i < NE; ++i) v = umax(v, hi[i]);
+    const uint32_t m = wave_umax(v);
+    if (m == 0) break;
+    uint64_t at[NE];
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      at[i] = __ballot(hi[i] == m);
+      n += __popcll(at[i]);
     }
-    __syncthreads();
-    if (in && !stays[g]) c[e] = ce = ninf;
-    __syncthreads();
-  }
-  int place = 1 << 30;
-  if (in) {
-    place = 0;
-    for (int j = 0; j < E; ++j) place += c[j] > ce || (c[j] == ce && j < e);
-  }
-  const bool some = ce > ninf;
-  if (place < a.topk) {
-    a.ids[t * a.topk + place] = some ? e : -1;
-    sel[place] = some ? s : 0.0;
-  }
-  __syncthreads();
-  if (place < a.topk) {
-    double w = some ? s : 0.0;
-    if (a.renormalise) {
-      double sum = 0.0;
-      for (int j = 0; j < a.topk; ++j) sum += sel[j];
-      w = sum > 0.0 ? w / sum : 0.0;
+    if (n > 1) {
+      v = 0;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) v = umax(v, hi[i] == m ? lo[i] : 0u);
+      const uint32_t ml = wave_umax(v);
+#pragma unroll
+      for (int i = 0; i < NE; ++i) at[i] = __ballot(hi[i] == m && lo[i] == ml);
     }
-    a.weights[t * a.topk + place] = (float)(w * a.scale);
+    int e = 0;
+#pragma unroll
+    for (int i = NE - 1; i >= 0; --i)
+      if (at[i]) e = i * 64 + __ffsll((unsigned long long)at[i]) - 1;
+    if (lane == j) mine = e;
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (i * 64 + lane == e) hi[i] = 0;
   }
+  double w = mine >= 0 ? lw[mine] : 0.0;
+  if (a.renormalise) {
+    double sum = 0.0;
+    for (int j = 0; j < a.topk; ++j) sum += lane_double(w, j);
+    w = sum > 0.0 ? w / sum : 0.0;
+  }
+  if (lane < a.topk) {
+    a.ids[t * a.topk + lane] = mine;
+    a.weights[t * a.topk + lane] = (float)(w * a.scale);
+  }
+}
+
+template <int NE>
+hipError_t route_launch(const RouteArgs& a, int64_t T, hipStream_t st) {
+  const size_t lds = (size_t)a.E * 16 + (a.n_group > 1 ? (size_t)a.n_group * 9 : 0);
+  hipLaunchKernelGGL((k_route_topk<NE>), dim3((unsigned)T), dim3(64), lds, st, a);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_route_topk(const RouteArgs& a, int64_t T, hipStream_t st) {
-  const unsigned nt = (unsigned)((a.E + 63) / 64 * 64);
-  hipLaunchKernelGGL(k_route_topk, dim3((unsigned)T), dim3(nt), 0, st, a);
-  return hipGetLastError();
+hipError_t launch_route_topk(RouteArgs a, int64_t T, hipStream_t st) {
+  const int per = a.E / a.n_group;
+  a.per_magic = (uint32_t)(((1 << 20) + per - 1) / per);
+  if (a.E <= 64) return route_launch<1>(a, T, st);
+  if (a.E <= 128) return route_launch<2>(a, T, st);
+  if (a.E <= 256) return route_launch<4>(a, T, st);
+  if (a.E <= 512) return route_launch<8>(a, T, st);
+  return route_launch<16>(a, T, st);
 }
 
 }  // namespace w8
