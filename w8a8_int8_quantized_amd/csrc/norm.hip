@@ -19,9 +19,6 @@
 namespace w8 {
 namespace {
 
-// Up to this many rows a row is spread over 1024 threads, one chunk each.
-constexpr int64_t kNormFewRows = 256;
-
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
@@ -93,8 +90,10 @@ struct Row {
 // t + NT, ... (CH of them at most), so the row is read once and stays in
 // registers through both norms and the quantiser.  A 128-value group is the
 // 16 chunks of 16 neighbouring lanes.
-template <bool FP16, int NT, int CH>
-__global__ __launch_bounds__(NT) void k_norm_residual_quant(NormArgs a) {
+// LATE: all but y is loaded where it is used instead, which leaves registers
+// for two workgroups of 1024 threads per CU.
+template <bool FP16, int NT, int CH, bool LATE>
+__global__ __launch_bounds__(NT, LATE ? 8 : 1) void k_norm_residual_quant(NormArgs a) {
   constexpr int NW = NT / 64;
   __shared__ float red[3][NW];
   const int64_t row = blockIdx.x;
@@ -103,13 +102,14 @@ __global__ __launch_bounds__(NT) void k_norm_residual_quant(NormArgs a) {
       pw(a.post_weight, 0, a.K), nw(a.pre_weight, 0, a.K);
   const float inv_k = 1.0f / (float)a.K;
 
-  uint4 raw[CH], rr[CH], rg[CH], rp[CH], rn[CH];
+  constexpr int CE = LATE ? 1 : CH;
+  uint4 raw[CH], rr[CE], rg[CE], rp[CE], rn[CE];
 #pragma unroll
   for (int i = 0; i < CH; ++i) raw[i] = y.chunk(threadIdx.x + NT * i);
 #pragma unroll
-  for (int i = 0; i < CH; ++i) rr[i] = res.chunk(threadIdx.x + NT * i);
+  for (int i = 0; i < CE && !LATE; ++i) rr[i] = res.chunk(threadIdx.x + NT * i);
 #pragma unroll
-  for (int i = 0; i < CH; ++i) {
+  for (int i = 0; i < CE && !LATE; ++i) {
     rg[i] = gate.chunk(threadIdx.x + NT * i);
     rp[i] = pw.chunk(threadIdx.x + NT * i);
     rn[i] = nw.chunk(threadIdx.x + NT * i);
@@ -133,16 +133,16 @@ __global__ __launch_bounds__(NT) void k_norm_residual_quant(NormArgs a) {
     float v[8], o[8];
     unpack8<FP16>(raw[i], v);
     if (a.post_weight) {
-      unpack8<FP16>(rp[i], o);
+      unpack8<FP16>(LATE ? pw.chunk(c) : rp[i % CE], o);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = v[e] * inv * o[e];
     }
     if (a.gate) {
-      unpack8<FP16>(rg[i], o);
+      unpack8<FP16>(LATE ? gate.chunk(c) : rg[i % CE], o);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] *= o[e];
     }
-    unpack8<FP16>(rr[i], o);   // zeros without a residual
+    unpack8<FP16>(LATE ? res.chunk(c) : rr[i % CE], o);   // zeros without a residual
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = v[e] * a.residual_scale + o[e];
     raw[i] = pack8<FP16>(v);
@@ -160,7 +160,7 @@ __global__ __launch_bounds__(NT) void k_norm_residual_quant(NormArgs a) {
     const int c = threadIdx.x + NT * i;
     float v[8], o[8];
     unpack8<FP16>(raw[i], v);
-    unpack8<FP16>(rn[i], o);
+    unpack8<FP16>(LATE ? nw.chunk(c) : rn[i % CE], o);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = v[e] * inv * o[e];
     raw[i] = pack8<FP16>(v);
@@ -192,20 +192,26 @@ __global__ __launch_bounds__(NT) void k_norm_residual_quant(NormArgs a) {
   if (!group && threadIdx.x == 0) a.q_scale[row] = make_scale(amax).s;
 }
 
-template <bool FP16, int NT, int CH>
+template <bool FP16, int NT, int CH, bool LATE = false>
 hipError_t norm_go(const NormArgs& a, int64_t M, hipStream_t st) {
-  hipLaunchKernelGGL((k_norm_residual_quant<FP16, NT, CH>), dim3((unsigned)M), dim3(NT), 0, st, a);
+  hipLaunchKernelGGL((k_norm_residual_quant<FP16, NT, CH, LATE>), dim3((unsigned)M), dim3(NT), 0, st, a);
   return hipGetLastError();
 }
 
+// Few rows leave CUs idle: the row is spread as thin as it goes.  With more
+// rows fewer and fuller threads win (K = 4096: 333 rows 6.2 us with 512
+// threads x 1 chunk against 6.4 with 256 x 2, 4096 rows 23.0 against 20.6).
 template <bool FP16>
 hipError_t norm_launch(const NormArgs& a, int64_t M, hipStream_t st) {
   const int nch = a.K >> 3;
-  if (nch > 1024) return norm_go<FP16, 1024, 4>(a, M, st);
-  if (M <= kNormFewRows) return nch <= 256 ? norm_go<FP16, 256, 1>(a, M, st) : norm_go<FP16, 1024, 1>(a, M, st);
+  const bool few = M <= 256;
   if (nch <= 256) return norm_go<FP16, 256, 1>(a, M, st);
-  if (nch <= 512) return norm_go<FP16, 256, 2>(a, M, st);
-  return norm_go<FP16, 256, 4>(a, M, st);
+  if (nch <= 512) return few ? norm_go<FP16, 512, 1>(a, M, st) : norm_go<FP16, 256, 2>(a, M, st);
+  if (nch <= 1024) return few ? norm_go<FP16, 1024, 1>(a, M, st) : norm_go<FP16, 512, 2>(a, M, st);
+  if (few) return nch <= 2048 ? norm_go<FP16, 1024, 2>(a, M, st) : norm_go<FP16, 1024, 4>(a, M, st);
+  if (nch <= 1536) return norm_go<FP16, 512, 3>(a, M, st);
+  if (nch <= 2048) return norm_go<FP16, 512, 4>(a, M, st);
+  return nch <= 3072 ? norm_go<FP16, 1024, 3, true>(a, M, st) : norm_go<FP16, 1024, 4, true>(a, M, st);
 }
 
 }  // namespace
