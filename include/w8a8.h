@@ -464,7 +464,7 @@ int moe_route_topk(const void* logits, int logits_dtype, const float* bias,
  *   to keep; it must not be used by other work until the stream has passed
  *   this call, so calls on different streams, or graphs that may run at the
  *   same time, need one each.
- * T <= 64, topk <= 16, E <= 4096, I and K multiples of 128 up to 2^17.
+ * T <= 64, topk <= 16, E <= 4096, I and K multiples of 128 up to 2^15.
  * Nothing is allocated; the call can be captured into a graph.
  */
 int64_t moe_workspace_bytes(int64_t T, int64_t topk, int64_t I);

@@ -73,9 +73,9 @@ def test_moe_argument_checks():
     assert _moe(T=65) == ESHAPE and _moe(T=-1) == ESHAPE
     assert _moe(topk=0) == ESHAPE and _moe(topk=17) == ESHAPE
     assert _moe(E=0) == ESHAPE and _moe(E=4097) == ESHAPE
-    assert _moe(I=0) == ESHAPE and _moe(I=100) == ESHAPE and _moe(I=(1 << 17) + 128) == ESHAPE
-    assert _moe(K=0) == ESHAPE and _moe(K=100) == ESHAPE and _moe(K=(1 << 17) + 128) == ESHAPE
-    assert _moe(E=4096, I=1 << 17, K=1 << 17) == ESHAPE
+    assert _moe(I=0) == ESHAPE and _moe(I=100) == ESHAPE and _moe(I=(1 << 15) + 128) == ESHAPE
+    assert _moe(K=0) == ESHAPE and _moe(K=100) == ESHAPE and _moe(K=(1 << 15) + 128) == ESHAPE
+    assert _moe(E=4096, I=1 << 15, K=1 << 15) == ESHAPE
     for name in ("A", "sa", "ids", "wt", "w13", "s13", "w2", "s2", "Y", "ws"):
         assert _moe(**{name: N}) == ENULL, name
     for name in ("A", "w13", "w2", "Y", "ws"):

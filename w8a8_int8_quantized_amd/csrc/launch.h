@@ -115,7 +115,7 @@ struct MoeArgs {
 };
 int64_t moe_workspace(int64_t T, int64_t topk, int64_t I, MoeArgs* a, void* ws);
 hipError_t launch_moe_block(const MoeArgs& a, OutKind out, hipStream_t st);
-constexpr int64_t kMoeMaxT = 64, kMoeMaxTopk = 16, kMoeMaxSide = 1 << 17, kMoeMaxE = 4096;
+constexpr int64_t kMoeMaxT = 64, kMoeMaxTopk = 16, kMoeMaxSide = 1 << 15, kMoeMaxE = 4096;
 
 // The library's own scratch (rules in workspace.h): at least `bytes` of
 // device memory for (current device, `st`, `slot`), slot 0 for split-K

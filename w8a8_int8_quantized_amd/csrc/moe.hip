@@ -30,7 +30,7 @@ using Int = std::integral_constant<int, N>;
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
 // Added to the offset of a load that must read zero: beyond the range of
-// every descriptor here (at most 1024 rows x 2^17 bytes), twice it still
+// every descriptor here (at most 1024 rows x 2^15 bytes), twice it still
 // inside 32 bits.
 constexpr uint32_t kOob = 0x40000000u;
 
@@ -65,53 +65,50 @@ __device__ __forceinline__ v4f block_fma(v4f acc, v4i w0, v4i w1, v4i a0, v4i a1
 // 4 (l >> 4) .. +3 of activation row l & 15.
 //
 // Sums over the K blocks par, par + WK, ... of rows r0 .. r0 + 16 MF - 1 of
-// expert e against its gate columns c0 .. c0 + 15 (acc[0]) and the up columns
-// of the same index (acc[1]).  PF blocks of loads stay in flight in a
-// register ring.
-template <int MF, int PF, int WK>
+// expert e against its gate columns c0 .. c0 + 16 FC - 1 (acc[f], f < FC) and
+// the up columns of the same index (acc[FC + f]).  PF blocks of loads stay in
+// flight in a register ring.  A CU's loads are limited by their number as
+// much as by their bytes, so the ring holds codes only: the scales of the
+// rows (sx, rows KB | 1 floats apart) and of the columns (sw, gate then up)
+// lie in LDS.
+template <int MF, int FC, int PF, int WK, class F>
 __device__ __forceinline__ void gate_up_sums(const MoeArgs& a, int e, int c0, int par, int r0, int n,
-                                             const uint16_t* tok, v4f (&acc)[2][MF]) {
+                                             const uint16_t* tok, const float* sx, const float* sw, F stage,
+                                             v4f (&acc)[2 * FC][MF]) {
   const int lane = threadIdx.x & 63;
   const int q = lane >> 4;
   const int K = a.K, KB = K >> 7;
   const int64_t wrow = (int64_t)e * 2 * a.I + c0;
-  const int64_t srow = (int64_t)e * 2 * (a.I >> 7) + (c0 >> 7);
-  const rsrc_t rg = rsrc(a.w13 + wrow * K, (int64_t)16 * K);
-  const rsrc_t ru = rsrc(a.w13 + (wrow + a.I) * K, (int64_t)16 * K);
-  const rsrc_t rsg = rsrc(a.s13 + srow * KB, (int64_t)KB * 4);
-  const rsrc_t rsu = rsrc(a.s13 + (srow + (a.I >> 7)) * KB, (int64_t)KB * 4);
+  const rsrc_t rg = rsrc(a.w13 + wrow * K, (int64_t)16 * FC * K);
+  const rsrc_t ru = rsrc(a.w13 + (wrow + a.I) * K, (int64_t)16 * FC * K);
   const rsrc_t ra = rsrc(a.A, (int64_t)a.T * K);
-  const rsrc_t rsa = rsrc(a.sa, (int64_t)a.T * KB * 4);
   const uint32_t woff = (uint32_t)((lane & 15) * K + q * 16);
-  uint32_t aoff[MF], saoff[MF];
+  uint32_t aoff[MF];
 #pragma unroll
   for (int j = 0; j < MF; ++j) {
     const int r = r0 + 16 * j + (lane & 15);
-    const uint32_t t = r < n ? tok[r] : 0u;
-    aoff[j] = r < n ? t * (uint32_t)K + q * 16 : kOob;
-    saoff[j] = r < n ? t * (uint32_t)KB * 4u : kOob;
+    aoff[j] = r < n ? (uint32_t)tok[r < n ? r : 0] * (uint32_t)K + q * 16 : kOob;
   }
 #pragma unroll
-  for (int f = 0; f < 2; ++f)
+  for (int f = 0; f < 2 * FC; ++f)
 #pragma unroll
     for (int j = 0; j < MF; ++j) acc[f][j] = (v4f){0.f, 0.f, 0.f, 0.f};
 
-  v4i wv[PF][2][2], av[PF][MF][2];
-  float sw[PF][2], sx[PF][MF];
+  v4i wv[PF][2 * FC][2], av[PF][MF][2];
   auto load = [&](int P, int kb) {
     const uint32_t ko = kb < KB ? (uint32_t)kb * 128u : kOob;
-    const uint32_t so = kb < KB ? (uint32_t)kb * 4u : kOob;
-    wv[P][0][0] = bl16(rg, woff + ko);
-    wv[P][0][1] = bl16(rg, woff + ko + 64);
-    wv[P][1][0] = bl16(ru, woff + ko);
-    wv[P][1][1] = bl16(ru, woff + ko + 64);
-    sw[P][0] = blf(rsg, so);
-    sw[P][1] = blf(rsu, so);
+#pragma unroll
+    for (int f = 0; f < FC; ++f) {
+      const uint32_t at = woff + (uint32_t)(16 * f * K) + ko;
+      wv[P][f][0] = bl16(rg, at);
+      wv[P][f][1] = bl16(rg, at + 64);
+      wv[P][FC + f][0] = bl16(ru, at);
+      wv[P][FC + f][1] = bl16(ru, at + 64);
+    }
 #pragma unroll
     for (int j = 0; j < MF; ++j) {
       av[P][j][0] = bl16(ra, aoff[j] + ko);
       av[P][j][1] = bl16(ra, aoff[j] + ko + 64);
-      sx[P][j] = blf(rsa, saoff[j] + so);
     }
   };
 #pragma unroll
@@ -119,16 +116,21 @@ __device__ __forceinline__ void gate_up_sums(const MoeArgs& a, int e, int c0, in
     load(p, par + WK * p);
     __builtin_amdgcn_sched_barrier(0);
   }
-  // blocks past the last hold zeros
+  stage();
+  // a block past the last multiplies zero codes, with the last one's scales
   for (int kb = par; kb < KB; kb += WK * PF) {
 #pragma unroll
     for (int p = 0; p < PF; ++p) {
+      const int kc = kb + WK * p < KB ? kb + WK * p : KB - 1;
+      const float sg = sw[kc], su = sw[KB + kc];
 #pragma unroll
-      for (int f = 0; f < 2; ++f)
+      for (int j = 0; j < MF; ++j) {
+        const float x = sx[(16 * j + (lane & 15)) * (KB | 1) + kc];
 #pragma unroll
-        for (int j = 0; j < MF; ++j)
+        for (int f = 0; f < 2 * FC; ++f)
           acc[f][j] = block_fma(acc[f][j], wv[p][f][0], wv[p][f][1], av[p][j][0], av[p][j][1],
-                                __fmul_rn(sx[p][j], sw[p][f]));
+                                __fmul_rn(x, f < FC ? sg : su));
+      }
       load(p, kb + WK * (p + PF));
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -265,64 +267,101 @@ __device__ __forceinline__ Chosen choose(const MoeArgs& a, int k, bool table, in
   return c;
 }
 
-// Grid (I / 16, min(pairs, E)): 16 columns of h of one expert per workgroup,
-// whose four waves split the K blocks.  A workgroup this small keeps the load
-// of the CUs even: each CU streams at a rate of its own (its outstanding
-// loads over the memory's latency), so the kernel takes as long as the CU
-// with the most bytes.  The 128 columns of a quantisation group lie in eight
-// workgroups; h leaves in fp32 and is quantised by its readers.
-template <int MF, int PF>
+// Grid (I / (16 FC), min(pairs, E)): 16 FC columns of h of one expert per
+// workgroup, whose four waves split the K blocks.  A workgroup this small
+// keeps the load of the CUs even: each CU streams at a rate of its own (its
+// outstanding loads over the memory's latency), so the kernel takes as long
+// as the CU with the most to load.  The 128 columns of a quantisation group
+// lie in several workgroups; h leaves in fp32 and is quantised by its readers.
+template <int MF, int FC, int PF>
 __device__ __forceinline__ void gate_up_rows(const MoeArgs& a, const Chosen& c, int r0, const uint16_t* tok,
                                              float* lds) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tile = blockIdx.x;
-  v4f acc[2][MF];
-  gate_up_sums<MF, PF, kGuWaves>(a, c.e, tile * 16, wave, r0, c.n, tok, acc);
+  const int c0 = blockIdx.x * 16 * FC;
+  const int KB = a.K >> 7;
+  float* sw = lds;
+  float* sx = sw + 2 * KB;
+  // the scales of the first 64 K blocks are on their way before the ring (a
+  // wait for a later load would wait for all of the ring's): wave 0 the gate
+  // columns', wave 1 the up columns', wave w the rows w, w + 4, ...; rows past
+  // the last read zeros
+  const rsrc_t rs = rsrc(a.s13 + (int64_t)c.e * 2 * (a.I >> 7) * KB, (int64_t)2 * (a.I >> 7) * KB * 4);
+  const rsrc_t rsa = rsrc(a.sa, (int64_t)a.T * KB * 4);
+  const uint32_t swoff = wave < 2 ? (uint32_t)((wave * (a.I >> 7) + (c0 >> 7)) * KB * 4) : kOob;
+  uint32_t sxoff[4 * MF];
+#pragma unroll
+  for (int j = 0; j < 4 * MF; ++j) {
+    const int r = r0 + wave + kGuWaves * j;
+    sxoff[j] = r < c.n ? (uint32_t)tok[r < c.n ? r : 0] * (uint32_t)KB * 4u : kOob;
+  }
+  float psw, psx[4 * MF];
+  auto fetch = [&](int i) {
+    const uint32_t o = i < KB ? (uint32_t)i * 4u : kOob;
+    psw = blf(rs, swoff + o);
+#pragma unroll
+    for (int j = 0; j < 4 * MF; ++j) psx[j] = blf(rsa, sxoff[j] + o);
+  };
+  fetch(lane);
+  auto stage = [&] {
+    for (int i = lane;; i += 64) {
+      if (i < KB) {
+        if (wave < 2) sw[wave * KB + i] = psw;
+#pragma unroll
+        for (int j = 0; j < 4 * MF; ++j) sx[(wave + kGuWaves * j) * (KB | 1) + i] = psx[j];
+      }
+      if (i - lane + 64 >= KB) break;
+      fetch(i + 64);
+    }
+    __syncthreads();
+  };
+  v4f acc[2 * FC][MF];
+  gate_up_sums<MF, FC, PF, kGuWaves>(a, c.e, c0, wave, r0, c.n, tok, sx, sw, stage, acc);
+  __syncthreads();   // the scales' place is free
   v4f* red = reinterpret_cast<v4f*>(lds);
   if (wave > 0) {
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
+    for (int f = 0; f < 2 * FC; ++f)
 #pragma unroll
-      for (int j = 0; j < MF; ++j) red[(((wave - 1) * 2 + f) * MF + j) * 64 + lane] = acc[f][j];
+      for (int j = 0; j < MF; ++j) red[(((wave - 1) * 2 * FC + f) * MF + j) * 64 + lane] = acc[f][j];
   }
   __syncthreads();
   if (wave == 0) {
 #pragma unroll
     for (int j = 0; j < MF; ++j) {
 #pragma unroll
-      for (int w = 0; w < kGuWaves - 1; ++w) {
-        acc[0][j] += red[((w * 2 + 0) * MF + j) * 64 + lane];
-        acc[1][j] += red[((w * 2 + 1) * MF + j) * 64 + lane];
-      }
+      for (int w = 0; w < kGuWaves - 1; ++w)
+#pragma unroll
+        for (int f = 0; f < 2 * FC; ++f) acc[f][j] += red[((w * 2 * FC + f) * MF + j) * 64 + lane];
       const int r = r0 + 16 * j + (lane & 15);
-      if (r < c.n)
-        *reinterpret_cast<v4f*>(a.h32 + (int64_t)(c.base + r) * a.I + tile * 16 + 4 * (lane >> 4)) =
-            silu_mul(acc[0][j], acc[1][j]);
+#pragma unroll
+      for (int f = 0; f < FC; ++f)
+        if (r < c.n)
+          *reinterpret_cast<v4f*>(a.h32 + (int64_t)(c.base + r) * a.I + c0 + 16 * f + 4 * (lane >> 4)) =
+              silu_mul(acc[f][j], acc[FC + f][j]);
     }
   }
   __syncthreads();
 }
 
-template <int MFMAX>
+// MFBIG: fragments of rows at a time for an expert of more than 16 rows.
+template <int MFBIG, int FC>
 __global__ __launch_bounds__(kGuThreads, 4) void k_moe_gate_up(MoeArgs a) {
   __shared__ uint16_t tok[kMaxPairs];
-  extern __shared__ float lds[];   // E ints, then the waves' sums
+  extern __shared__ float lds[];   // E ints, then the scales, then the waves' sums
   const Chosen c = choose(a, blockIdx.y, blockIdx.x == 0, reinterpret_cast<int*>(lds), tok);
   if (c.e < 0) return;
-  // a token that names an expert twice gives it two rows, so n can pass T:
-  // the rows past 16 MFMAX take further passes over the weights
-  auto rows = [&](auto mf, auto pf) {
-    for (int r0 = 0; r0 < c.n; r0 += 16 * mf()) gate_up_rows<mf(), pf()>(a, c, r0, tok, lds);
-  };
-  if (MFMAX == 1 || c.n <= 16) rows(Int<1>(), Int<3>());
-  else if (MFMAX == 2 || c.n <= 32) rows(Int<MFMAX < 2 ? MFMAX : 2>(), Int<2>());
-  else rows(Int<MFMAX>(), Int<1>());
+  if (c.n <= 16) {
+    gate_up_rows<1, FC, FC == 1 ? 4 : 2>(a, c, 0, tok, lds);
+  } else {
+    for (int r0 = 0; r0 < c.n; r0 += 16 * MFBIG) gate_up_rows<MFBIG, FC, 1>(a, c, r0, tok, lds);
+  }
 }
 
 // The codes and scales of h, a group per 8 lanes; rows behind the last pair's
 // hold whatever the workspace held and nobody reads theirs.
-__global__ __launch_bounds__(256) void k_moe_quant(MoeArgs a, int groups) {
+__global__ __launch_bounds__(256) void k_moe_quant(MoeArgs a, int P, int IB) {
+  const int groups = P * IB;
   const int g = blockIdx.x * 32 + (threadIdx.x >> 3), l8 = threadIdx.x & 7;
   const float4* at = reinterpret_cast<const float4*>(a.h32 + (int64_t)(g < groups ? g : groups - 1) * 128) + l8 * 4;
   float v[16], s;
@@ -337,7 +376,7 @@ __global__ __launch_bounds__(256) void k_moe_quant(MoeArgs a, int groups) {
   const uint4 o = quant16(v, &s);
   if (g < groups) {
     reinterpret_cast<uint4*>(a.hq + (int64_t)g * 128)[l8] = o;
-    if (l8 == 0) a.hs[g] = s;
+    if (l8 == 0) a.hs[(int64_t)(g % IB) * P + g / IB] = s;
   }
 }
 
@@ -353,6 +392,9 @@ __global__ __launch_bounds__(256) void k_moe_quant(MoeArgs a, int groups) {
 // every time.
 constexpr int kDownWaves = 8, kDownThreads = 64 * kDownWaves;
 
+// Pairs whose h every down workgroup quantises for itself, at most.
+constexpr int64_t kLdsPairs = 64, kLdsCodes = 32768;
+
 // LDSH (few pairs): every workgroup quantises the h of all pairs into LDS
 // (rows of I + 16 bytes, so that the 16 rows of a fragment read lie in
 // different banks) while its first weights are on their way; else k_moe_quant
@@ -362,7 +404,7 @@ __global__ __launch_bounds__(kDownThreads, 2) void k_moe_down(MoeArgs a, int cw,
   // smax [P][16 FN] results; units (expert, first row, rows); pos and weight
   // per pair; LDSH: scales [P][I / 128] and codes [P][I + 16]
   extern __shared__ float lds[];
-  __shared__ int units_s;
+  __shared__ int units_s;   // (not LDSH)
   const int lane = threadIdx.x & 63, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n0 = blockIdx.x * cw, cols = a.K - n0 < cw ? a.K - n0 : cw;
@@ -377,46 +419,92 @@ __global__ __launch_bounds__(kDownThreads, 2) void k_moe_down(MoeArgs a, int cw,
   // h of the first groups, 8 lanes to a group (rows behind the last one hold
   // anything, and nobody reads their codes)
   const int l8 = threadIdx.x & 7, g0 = threadIdx.x >> 3;
-  float4 raw[4];
-  auto fetch = [&](int g) {
-    const float4* at = reinterpret_cast<const float4*>(a.h32 + (int64_t)(g < P * IB ? g : 0) * 128) + l8 * 4;
+  constexpr int kPasses = LDSH ? kLdsCodes / 128 / (kDownThreads / 8) : 1;
+  float4 raw[kPasses][4];
+  if constexpr (LDSH) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) raw[i] = at[i];
-  };
-  if (LDSH) fetch(g0);
-
-  // the list of units, by the first wave; pos and weights, by the others
-  if (wave == 0) {
-    int units = 0;
-    for (int c = 0; c < most; c += 64) {
-      const int k = c + lane;
-      const int n = k < most ? a.count[k] : 0, e = k < most ? a.expert[k] : 0, b = k < most ? a.start[k] : 0;
-      const int tiles = (n + 16 * MF - 1) / (16 * MF);
-      int inc = tiles;
+    for (int k = 0; k < kPasses; ++k) {
+      const int g = g0 + k * (kDownThreads / 8);
+      if (k * (kDownThreads / 8) >= P * IB) break;
+      const float4* at = reinterpret_cast<const float4*>(a.h32 + (int64_t)(g < P * IB ? g : 0) * 128) + l8 * 4;
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int v = __shfl_up(inc, d, 64);
-        if (lane >= d) inc += v;
-      }
-      for (int i = 0; i < tiles; ++i) {
-        const int u = units + inc - tiles + i;
-        ue[u] = (uint16_t)e;
-        ub[u] = (uint16_t)(b + i * 16 * MF);
-        un[u] = (uint16_t)(n - i * 16 * MF < 16 * MF ? n - i * 16 * MF : 16 * MF);
-      }
-      units += __builtin_amdgcn_readlane(inc, 63);
-    }
-    if (lane == 0) units_s = units;
-  } else {
-    for (int p = threadIdx.x - 64; p < P; p += kDownThreads - 64) {
-      pos[p] = a.pos[p];
-      wt[p] = a.weights[p];
+      for (int i = 0; i < 4; ++i) raw[k][i] = at[i];
     }
   }
-  for (int i = threadIdx.x; i < smax * P * 4 * FN; i += kDownThreads)
-    reinterpret_cast<float4*>(lds)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  __syncthreads();
-  const int units = __builtin_amdgcn_readfirstlane(units_s);
+
+  // the units in the order of the chosen experts.  LDSH: at most 64 experts,
+  // one to a lane, in every wave's registers (inc: units up to and with this
+  // expert's), so that nothing stands between the tables and the first
+  // weights; else a list in LDS, by the first wave
+  auto tiles_of = [](int n) { return (n + 16 * MF - 1) / (16 * MF); };
+  auto scan = [&](int v) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(v, d, 64);
+      if (lane >= d) v += o;
+    }
+    return v;
+  };
+  int units, n_l = 0, e_l = 0, b_l = 0, inc = 0, pos_l = 0;
+  float wt_l = 0.f;
+  if constexpr (LDSH) {
+    if (lane < most) {
+      n_l = a.count[lane];
+      e_l = a.expert[lane];
+      b_l = a.start[lane];
+    }
+    if ((int)threadIdx.x < P) {
+      pos_l = a.pos[threadIdx.x];
+      wt_l = a.weights[threadIdx.x];
+    }
+    inc = scan(tiles_of(n_l));
+    units = __builtin_amdgcn_readlane(inc, 63);
+  } else {
+    if (wave == 0) {
+      int u0 = 0;
+      for (int c = 0; c < most; c += 64) {
+        const int k = c + lane;
+        const int n = k < most ? a.count[k] : 0, e = k < most ? a.expert[k] : 0, b = k < most ? a.start[k] : 0;
+        const int t = tiles_of(n), end = scan(t);
+        for (int i = 0; i < t; ++i) {
+          const int u = u0 + end - t + i;
+          ue[u] = (uint16_t)e;
+          ub[u] = (uint16_t)(b + i * 16 * MF);
+          un[u] = (uint16_t)(n - i * 16 * MF < 16 * MF ? n - i * 16 * MF : 16 * MF);
+        }
+        u0 += __builtin_amdgcn_readlane(end, 63);
+      }
+      if (lane == 0) units_s = u0;
+    } else {
+      for (int p = threadIdx.x - 64; p < P; p += kDownThreads - 64) {
+        pos[p] = a.pos[p];
+        wt[p] = a.weights[p];
+      }
+    }
+    for (int i = threadIdx.x; i < smax * P * 4 * FN; i += kDownThreads)
+      reinterpret_cast<float4*>(lds)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();
+    units = __builtin_amdgcn_readfirstlane(units_s);
+  }
+  struct Unit {
+    int e, base, rows;
+  };
+  auto unit = [&](int u) {
+    Unit r;
+    if constexpr (LDSH) {
+      const int k = __ffsll((unsigned long long)__ballot(inc > u)) - 1;
+      const int n = __builtin_amdgcn_readlane(n_l, k);
+      const int r0 = (u - (__builtin_amdgcn_readlane(inc, k) - tiles_of(n))) * 16 * MF;
+      r.e = __builtin_amdgcn_readlane(e_l, k);
+      r.base = __builtin_amdgcn_readlane(b_l, k) + r0;
+      r.rows = n - r0 < 16 * MF ? n - r0 : 16 * MF;
+    } else {
+      r.e = __builtin_amdgcn_readfirstlane(ue[u]);
+      r.base = __builtin_amdgcn_readfirstlane(ub[u]);
+      r.rows = __builtin_amdgcn_readfirstlane(un[u]);
+    }
+    return r;
+  };
 
   const int G = (IB + smax - 1) / smax, per = (IB + G - 1) / G;   // blocks per granule, granules per unit
   const int lo = (int)((int64_t)units * per * wave / kDownWaves);
@@ -428,19 +516,16 @@ __global__ __launch_bounds__(kDownThreads, 2) void k_moe_down(MoeArgs a, int cw,
   // the unit being loaded and the next block of it
   int lu = lo / per, lkb = lo % per * G;
   rsrc_t rw, rsw, rh, rhs;
-  int lbase = 0, lrows = 0;
   auto open = [&](int u) {
-    const int e = __builtin_amdgcn_readfirstlane(ue[u]);
-    lbase = __builtin_amdgcn_readfirstlane(ub[u]);
-    lrows = __builtin_amdgcn_readfirstlane(un[u]);
-    rw = rsrc(a.w2 + ((int64_t)e * a.K + n0) * I, (int64_t)cols * I);
-    rsw = rsrc(a.s2 + (int64_t)e * (a.K >> 7) * IB, (int64_t)(a.K >> 7) * IB * 4);
+    const Unit c = unit(u);
+    rw = rsrc(a.w2 + ((int64_t)c.e * a.K + n0) * I, (int64_t)cols * I);
+    rsw = rsrc(a.s2 + (int64_t)c.e * (a.K >> 7) * IB, (int64_t)(a.K >> 7) * IB * 4);
     if (!LDSH) {
-      rh = rsrc(a.hq + (int64_t)lbase * I, (int64_t)lrows * I);
-      rhs = rsrc(a.hs + (int64_t)lbase * IB, (int64_t)lrows * IB * 4);
+      rh = rsrc(a.hq + (int64_t)c.base * I, (int64_t)c.rows * I);
+      rhs = rsrc(a.hs + c.base, ((int64_t)(IB - 1) * P + c.rows) * 4);
     }
   };
-  const uint32_t off = (uint32_t)((lane & 15) * I + q * 16), soff = (uint32_t)((lane & 15) * IB * 4);
+  const uint32_t off = (uint32_t)((lane & 15) * I + q * 16), soff = (uint32_t)((lane & 15) * 4);
   // the result lane's four columns lie in one 128-row block of the weights
   uint32_t swoff[FN];
 #pragma unroll
@@ -463,7 +548,7 @@ __global__ __launch_bounds__(kDownThreads, 2) void k_moe_down(MoeArgs a, int cw,
       for (int j = 0; j < MF; ++j) {
         av[S][j][0] = bl16(rh, off + (uint32_t)(16 * j * I) + ko);
         av[S][j][1] = bl16(rh, off + (uint32_t)(16 * j * I) + ko + 64);
-        sx[S][j] = blf(rhs, soff + (uint32_t)(16 * j * IB * 4) + so);
+        sx[S][j] = blf(rhs, soff + (uint32_t)(64 * j) + (left > 0 ? so * (uint32_t)P : kOob));
       }
     }
     --left;
@@ -480,15 +565,23 @@ __global__ __launch_bounds__(kDownThreads, 2) void k_moe_down(MoeArgs a, int cw,
     __builtin_amdgcn_sched_barrier(0);
   }
   if constexpr (LDSH) {
-    for (int g = g0; g - g0 < P * IB; g += kDownThreads / 8) {
-      if (g != g0) fetch(g);
+    if ((int)threadIdx.x < P) {
+      pos[threadIdx.x] = pos_l;
+      wt[threadIdx.x] = wt_l;
+    }
+    for (int i = threadIdx.x; i < smax * P * 4 * FN; i += kDownThreads)
+      reinterpret_cast<float4*>(lds)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kPasses; ++k) {
+      const int g = g0 + k * (kDownThreads / 8);
+      if (k * (kDownThreads / 8) >= P * IB) break;
       float v[16], s;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[4 * i] = raw[i].x;
-        v[4 * i + 1] = raw[i].y;
-        v[4 * i + 2] = raw[i].z;
-        v[4 * i + 3] = raw[i].w;
+        v[4 * i] = raw[k][i].x;
+        v[4 * i + 1] = raw[k][i].y;
+        v[4 * i + 2] = raw[k][i].z;
+        v[4 * i + 3] = raw[k][i].w;
       }
       const uint4 o = quant16(v, &s);
       if (g < P * IB) {
@@ -504,8 +597,9 @@ __global__ __launch_bounds__(kDownThreads, 2) void k_moe_down(MoeArgs a, int cw,
   int u = lo / per, kb = lo % per * G, place = lo % per;
   int base = 0, rows = 0;
   auto take = [&] {
-    base = __builtin_amdgcn_readfirstlane(ub[u]);
-    rows = __builtin_amdgcn_readfirstlane(un[u]);
+    const Unit c = unit(u);
+    base = c.base;
+    rows = c.rows;
   };
   if (todo > 0) take();
   v4f acc[FN][MF];
@@ -576,9 +670,6 @@ __global__ __launch_bounds__(kDownThreads, 2) void k_moe_down(MoeArgs a, int cw,
   }
 }
 
-// Pairs whose h every down workgroup quantises for itself, at most.
-constexpr int64_t kLdsPairs = 64, kLdsCodes = 32768;
-
 bool quant_in_down(int64_t P, int64_t I) { return P <= kLdsPairs && P * I <= kLdsCodes; }
 
 // Columns per down workgroup: a multiple of 4 up to 32, the widest of those
@@ -601,8 +692,10 @@ hipError_t down_launch(const MoeArgs& a, OutKind out, int cw, int most, hipStrea
   const size_t res = (size_t)P * FN * 64;
   const size_t rest = (size_t)(P * 14 + 15) / 16 * 16 +
                       (LDSH ? (size_t)(P * IB + 3) / 4 * 16 + (size_t)P * (a.I + 16) : 0);
+  // a unit is cut for several waves only where units are few or large
+  const int cuts = 4 * P >= kDownWaves ? 4 : kDownWaves;
   int smax = 1;
-  while (smax * 2 <= IB && smax * 2 <= kDownWaves && smax * 2 * res + rest <= 131072) smax *= 2;
+  while (smax * 2 <= IB && smax * 2 <= cuts && smax * 2 * res + rest <= 131072) smax *= 2;
   const dim3 grid((unsigned)((a.K + cw - 1) / cw)), block(kDownThreads);
   const size_t lds = smax * res + rest;
   if (out == OUT_F32)
@@ -612,11 +705,15 @@ hipError_t down_launch(const MoeArgs& a, OutKind out, int cw, int most, hipStrea
   return hipGetLastError();
 }
 
-template <int MFMAX>
+template <int MFBIG, int FC>
 hipError_t gate_up_launch(const MoeArgs& a, int most, hipStream_t st) {
-  const size_t sums = (size_t)(kGuWaves - 1) * 2 * MFMAX * 1024, owner = (size_t)a.E * 4;
-  hipLaunchKernelGGL((k_moe_gate_up<MFMAX>), dim3((unsigned)(a.I / 16), (unsigned)most), dim3(kGuThreads),
-                     sums > owner ? sums : owner, st, a);
+  const int KB = a.K >> 7;
+  const size_t sums = (size_t)(kGuWaves - 1) * 2 * FC * MFBIG * 1024, owner = (size_t)a.E * 4;
+  const size_t scales = ((size_t)2 * KB + (size_t)16 * MFBIG * (KB | 1)) * 4;
+  size_t lds = sums > owner ? sums : owner;
+  if (scales > lds) lds = scales;
+  hipLaunchKernelGGL((k_moe_gate_up<MFBIG, FC>), dim3((unsigned)(a.I / (16 * FC)), (unsigned)most), dim3(kGuThreads),
+                     lds, st, a);
   return hipGetLastError();
 }
 
@@ -648,15 +745,16 @@ int64_t moe_workspace(int64_t T, int64_t topk, int64_t I, MoeArgs* a, void* ws) 
 hipError_t launch_moe_block(const MoeArgs& a, OutKind out, hipStream_t st) {
   const int P = a.T * a.topk, IB = a.I / 128;
   const int most = P < a.E ? P : a.E;   // chosen experts, at most
-  hipError_t e = a.T <= 16   ? gate_up_launch<1>(a, most, st)
-                 : a.T <= 32 ? gate_up_launch<2>(a, most, st)
-                             : gate_up_launch<4>(a, most, st);
+  const bool wide = (int64_t)(a.I / 32) * most >= 256;
+  hipError_t e = P > 12 * a.E ? gate_up_launch<4, 1>(a, most, st)
+                 : wide       ? gate_up_launch<2, 2>(a, most, st)
+                              : gate_up_launch<2, 1>(a, most, st);
   if (e != hipSuccess) return e;
   const int cw = down_columns(a.K);
   if (quant_in_down(P, a.I))
     return cw <= 16 ? down_launch<1, 1, 8, true>(a, out, cw, most, st)
                     : down_launch<1, 2, 6, true>(a, out, cw, most, st);
-  hipLaunchKernelGGL(k_moe_quant, dim3((unsigned)((P * IB + 31) / 32)), dim3(256), 0, st, a, P * IB);
+  hipLaunchKernelGGL(k_moe_quant, dim3((unsigned)((P * IB + 31) / 32)), dim3(256), 0, st, a, P, IB);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   // rows per unit by the mean rows of an expert (a unit of more rows than its
