@@ -454,12 +454,12 @@ int moe_route_topk(const void* logits, int logits_dtype, const float* bias,
  *   A [T][K] int8, a_scale [T][K/128]   (quant_act_group, norm_residual_quant)
  *   topk_ids [T][topk] int32 DEVICE array, topk_weights [T][topk] fp32: a slot
  *   whose id is outside 0 .. E - 1 (an expert of another GPU, a masked slot,
- *   a padding row) adds nothing and its weight is not read; a token without
+ *   a padding row) adds nothing, whatever its weight; a token without
  *   any slot gets a row of zeros; a token may name an expert twice
  *   W_gate_up [E][2 I][K] int8 (gate rows first), gate_up_scale [E][2 I/128][K/128]
  *   W_down    [E][K][I]   int8,                   down_scale    [E][K/128][I/128]
  *   Y [T][K] bf16 or fp32 (y_dtype)
- *   workspace: caller-owned device memory of moe_workspace_bytes(T, topk, I)
+ *   workspace: caller-owned device memory of moe_workspace_bytes(T, topk, I, K)
  *   bytes (fewer gives W8_ERR_WORKSPACE), 256-byte aligned, with no contents
  *   to keep; it must not be used by other work until the stream has passed
  *   this call, so calls on different streams, or graphs that may run at the
@@ -467,7 +467,7 @@ int moe_route_topk(const void* logits, int logits_dtype, const float* bias,
  * T <= 64, topk <= 16, E <= 4096, I and K multiples of 128 up to 2^15.
  * Nothing is allocated; the call can be captured into a graph.
  */
-int64_t moe_workspace_bytes(int64_t T, int64_t topk, int64_t I);
+int64_t moe_workspace_bytes(int64_t T, int64_t topk, int64_t I, int64_t K);
 
 int moe_w8a8_block(const int8_t* A, const float* a_scale, const int32_t* topk_ids,
                    const float* topk_weights, const int8_t* W_gate_up,

@@ -279,7 +279,7 @@ def _to(args):
     (1, 1, 1, 128, 128), (1, 2, 4, 256, 384), (1, 8, 16, 128, 1024), (2, 3, 5, 384, 256), (3, 16, 20, 128, 128),
     (5, 2, 3, 640, 256), (7, 6, 8, 256, 640), (16, 2, 4, 128, 256), (17, 4, 4, 256, 128), (20, 1, 1, 128, 256),
     (32, 3, 6, 128, 384), (33, 2, 2, 256, 256), (48, 1, 1, 384, 128), (64, 8, 12, 128, 256), (64, 1, 1, 256, 128),
-    (64, 16, 40, 128, 128), (1, 1, 300, 128, 128), (4, 2, 8, 1152, 128), (3, 1, 2, 128, 2176)])
+    (64, 16, 40, 128, 128), (40, 5, 24, 384, 1280), (64, 2, 3, 1024, 384), (33, 8, 64, 128, 2176), (1, 1, 300, 128, 128), (4, 2, 8, 1152, 128), (3, 1, 2, 128, 2176)])
 def test_moe(T, topk, E, I, K):
     print(f"moe T={T} topk={topk} E={E} I={I} K={K}", flush=True)
     args = _moe_inputs(T, topk, E, I, K, seed=T + E + I)
@@ -307,7 +307,7 @@ def test_moe_empty_slots_and_repeats():
     args = _moe_inputs(T, topk, E, I, K, seed=2, ids=ids)
     args[3][(ids < 0) | (ids >= E)] = np.nan
     t = _to(args)
-    ws = torch.full((w8.moe_workspace_bytes(T, topk, I),), 0xFF, dtype=torch.uint8, device=DEV)
+    ws = torch.full((w8.moe_workspace_bytes(T, topk, I, K),), 0xFF, dtype=torch.uint8, device=DEV)
     buf = torch.full((T + 1, K), 5.0, device=DEV)
     got = w8.moe_w8a8_block(*t, out=buf[:T], workspace=ws)
     _check_moe(args, got, w8.moe_w8a8_block(*t))
@@ -400,7 +400,7 @@ def test_layer_graph_replays_and_streams():
     work between the replays; and two streams at once with a workspace each."""
     K, I, E, T = 512, 256, 16, 24
     _, p = _step_params(K, I, E, seed=30)
-    ws = torch.empty(w8.moe_workspace_bytes(T, 4, I), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(w8.moe_workspace_bytes(T, 4, I, K), dtype=torch.uint8, device=DEV)
     xs = [synth.activations(T, K, seed=40 + i).to(DEV) for i in range(4)]
     r = synth.activations(T, K, seed=50).to(DEV)
     want = [_step(x, r, p, None) for x in xs]

@@ -82,12 +82,13 @@ def test_moe_argument_checks():
         assert _moe(**{name: P4}) == EALIGN, name
     for name in ("sa", "ids", "wt", "s13", "s2"):
         assert _moe(**{name: P2}) == EALIGN, name
-    need = w8.lib.moe_workspace_bytes(4, 2, 256)
+    need = w8.lib.moe_workspace_bytes(4, 2, 256, 256)
     assert need > 4 * 2 * (256 + 4 * 2)
     assert _moe(nbytes=need - 1) == EWS
     assert _moe(T=0, A=N, Y=N, ws=N, nbytes=0) == OK
-    assert w8.lib.moe_workspace_bytes(65, 2, 256) == ESHAPE
-    assert w8.lib.moe_workspace_bytes(4, 2, 200) == ESHAPE
+    assert w8.lib.moe_workspace_bytes(65, 2, 256, 256) == ESHAPE
+    assert w8.lib.moe_workspace_bytes(4, 2, 200, 256) == ESHAPE
+    assert w8.lib.moe_workspace_bytes(4, 2, 256, 200) == ESHAPE
 
 
 def test_binding_refuses_cpu_tensors_and_wrong_shapes():

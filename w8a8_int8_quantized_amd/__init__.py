@@ -96,7 +96,7 @@ _FUNCS = {
                             + [ctypes.c_void_p] * 5),
     "moe_route_topk": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
                                       ctypes.c_int64] + [ctypes.c_int] * 5 + [ctypes.c_double] + [ctypes.c_void_p] * 3),
-    "moe_workspace_bytes": (ctypes.c_int64, [ctypes.c_int64] * 3),
+    "moe_workspace_bytes": (ctypes.c_int64, [ctypes.c_int64] * 4),
     "moe_w8a8_block": (ctypes.c_int, [ctypes.c_void_p] * 9 + [ctypes.c_int] + [ctypes.c_int64] * 5
                        + [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
 }
@@ -532,9 +532,9 @@ def moe_route_topk(logits, topk, bias=None, score=W8_ROUTE_SOFTMAX, n_group=1, t
 
 
 @functools.lru_cache(maxsize=256)
-def moe_workspace_bytes(T, topk, I):
+def moe_workspace_bytes(T, topk, I, K):
     """Bytes of workspace moe_w8a8_block needs."""
-    n = lib.moe_workspace_bytes(T, topk, I)
+    n = lib.moe_workspace_bytes(T, topk, I, K)
     _check(min(n, 0), "moe_workspace_bytes")
     return n
 
@@ -549,7 +549,7 @@ def moe_w8a8_block(A, a_scale, topk_ids, topk_weights, W_gate_up, gate_up_scale,
     outside 0 .. E-1 add nothing); W_gate_up int8 [E, 2I, K] (gate rows first)
     with gate_up_scale [E, 2I/128, K/128]; W_down int8 [E, K, I] with
     down_scale [E, K/128, I/128].  workspace: uint8, moe_workspace_bytes(T,
-    topk, I) or more; without one, torch allocates it for the call.
+    topk, I, K) or more; without one, torch allocates it for the call.
     """
     _dev(A)
     T, K = A.shape
@@ -570,7 +570,7 @@ def moe_w8a8_block(A, a_scale, topk_ids, topk_weights, W_gate_up, gate_up_scale,
     if out.dtype not in (torch.bfloat16, torch.float32):
         raise W8Error(f"moe_w8a8_block writes bf16 or fp32, not {out.dtype}")
     if workspace is None:
-        workspace = torch.empty((moe_workspace_bytes(T, topk, I),), dtype=torch.uint8, device=dev)
+        workspace = torch.empty((moe_workspace_bytes(T, topk, I, K),), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise W8Error(f"workspace must be contiguous, on {dev}")
     _run_on(dev, "moe_w8a8_block", lib.moe_w8a8_block, A.data_ptr(), a_scale.data_ptr(), topk_ids.data_ptr(),

@@ -426,15 +426,16 @@ int moe_route_topk(const void* logits, int logits_dtype, const float* bias, int 
 }
 
 // The size rules of the few-token layer, shared by the call and its workspace query.
-static int check_moe(int64_t T, int64_t topk, int64_t I) {
+static int check_moe(int64_t T, int64_t topk, int64_t I, int64_t K) {
   if (T < 0 || T > w8::kMoeMaxT || topk < 1 || topk > w8::kMoeMaxTopk) return W8_ERR_SHAPE;
   if (I < 128 || I > w8::kMoeMaxSide || (I & 127) != 0) return W8_ERR_SHAPE;
+  if (K < 128 || K > w8::kMoeMaxSide || (K & 127) != 0) return W8_ERR_SHAPE;
   return W8_OK;
 }
 
-int64_t moe_workspace_bytes(int64_t T, int64_t topk, int64_t I) {
-  int rc = check_moe(T, topk, I);
-  return rc ? rc : w8::moe_workspace(T, topk, I, nullptr, nullptr);
+int64_t moe_workspace_bytes(int64_t T, int64_t topk, int64_t I, int64_t K) {
+  int rc = check_moe(T, topk, I, K);
+  return rc ? rc : w8::moe_workspace(T, topk, I, K, nullptr, nullptr);
 }
 
 int moe_w8a8_block(const int8_t* A, const float* a_scale, const int32_t* topk_ids, const float* topk_weights,
@@ -444,9 +445,9 @@ int moe_w8a8_block(const int8_t* A, const float* a_scale, const int32_t* topk_id
   w8::OutKind out;
   int rc = check_out(y_dtype, false, &out);
   if (rc) return rc;
-  rc = check_moe(T, topk, I);
+  rc = check_moe(T, topk, I, K);
   if (rc) return rc;
-  if (E < 1 || E > w8::kMoeMaxE || K < 128 || K > w8::kMoeMaxSide || (K & 127) != 0) return W8_ERR_SHAPE;
+  if (E < 1 || E > w8::kMoeMaxE) return W8_ERR_SHAPE;
   if (2 * I * K > kMaxElems / E) return W8_ERR_SHAPE;
   if (T == 0) return W8_OK;
   if (!A || !a_scale || !topk_ids || !topk_weights || !W_gate_up || !gate_up_scale || !W_down || !down_scale || !Y ||
@@ -456,7 +457,7 @@ int moe_w8a8_block(const int8_t* A, const float* a_scale, const int32_t* topk_id
       !aligned(workspace, 256) || !aligned(a_scale, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) ||
       !aligned(gate_up_scale, 4) || !aligned(down_scale, 4))
     return W8_ERR_ALIGN;
-  if (workspace_bytes < w8::moe_workspace(T, topk, I, nullptr, nullptr)) return W8_ERR_WORKSPACE;
+  if (workspace_bytes < w8::moe_workspace(T, topk, I, K, nullptr, nullptr)) return W8_ERR_WORKSPACE;
   w8::MoeArgs a;
   a.A = A;
   a.sa = a_scale;
@@ -472,7 +473,7 @@ int moe_w8a8_block(const int8_t* A, const float* a_scale, const int32_t* topk_id
   a.E = (int)E;
   a.I = (int)I;
   a.K = (int)K;
-  w8::moe_workspace(T, topk, I, &a, workspace);
+  w8::moe_workspace(T, topk, I, K, &a, workspace);
   return status_of(w8::launch_moe_block(a, out, as_stream(stream)));
 }
 

@@ -94,7 +94,7 @@ struct RouteArgs {
 hipError_t launch_route_topk(RouteArgs a, int64_t T, hipStream_t st);
 constexpr int64_t kRouteMaxE = 1024, kRouteMaxTopk = 64;
 
-// A mixture-of-experts layer for a few tokens (moe.hip).  h32 .. start lie in
+// A mixture-of-experts layer for a few tokens (moe.hip).  h32 .. start (out32 among them) lie in
 // the caller's workspace: moe_workspace gives its size and, with a and ws,
 // sets them.
 struct MoeArgs {
@@ -109,11 +109,11 @@ struct MoeArgs {
   void* Y;
   float* h32;
   int8_t* hq;
-  float* hs;
+  float *hs, *out32;
   int32_t *pos, *expert, *count, *start;
   int T, topk, E, I, K;
 };
-int64_t moe_workspace(int64_t T, int64_t topk, int64_t I, MoeArgs* a, void* ws);
+int64_t moe_workspace(int64_t T, int64_t topk, int64_t I, int64_t K, MoeArgs* a, void* ws);
 hipError_t launch_moe_block(const MoeArgs& a, OutKind out, hipStream_t st);
 constexpr int64_t kMoeMaxT = 64, kMoeMaxTopk = 16, kMoeMaxSide = 1 << 15, kMoeMaxE = 4096;
 

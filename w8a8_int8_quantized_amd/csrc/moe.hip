@@ -267,18 +267,21 @@ __device__ __forceinline__ Chosen choose(const MoeArgs& a, int k, bool table, in
   return c;
 }
 
-// Grid (I / (16 FC), min(pairs, E)): 16 FC columns of h of one expert per
-// workgroup, whose four waves split the K blocks.  A workgroup this small
-// keeps the load of the CUs even: each CU streams at a rate of its own (its
-// outstanding loads over the memory's latency), so the kernel takes as long
-// as the CU with the most to load.  The 128 columns of a quantisation group
-// lie in several workgroups; h leaves in fp32 and is quantised by its readers.
-template <int MF, int FC, int PF>
+// Grid (I / (16 FC 4 / WK), min(pairs, E)).  The four waves of a workgroup
+// split 16 FC 4 / WK columns of h of one expert, WK of them sharing 16 FC
+// columns and splitting the K blocks.  A workgroup this small keeps the load
+// of the CUs even: each CU streams at a rate of its own (its outstanding
+// loads over the memory's latency), so the kernel takes as long as the CU
+// with the most to load.  The 128 columns of a quantisation group may lie in
+// several workgroups; h leaves in fp32 and is quantised by its readers.
+template <int MF, int FC, int PF, int WK>
 __device__ __forceinline__ void gate_up_rows(const MoeArgs& a, const Chosen& c, int r0, const uint16_t* tok,
                                              float* lds) {
+  constexpr int TILES = kGuWaves / WK;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c0 = blockIdx.x * 16 * FC;
+  const int part = wave % WK, tile = wave / WK;
+  const int c0 = (blockIdx.x * TILES + tile) * 16 * FC;
   const int KB = a.K >> 7;
   float* sw = lds;
   float* sx = sw + 2 * KB;
@@ -316,23 +319,29 @@ __device__ __forceinline__ void gate_up_rows(const MoeArgs& a, const Chosen& c, 
     __syncthreads();
   };
   v4f acc[2 * FC][MF];
-  gate_up_sums<MF, FC, PF, kGuWaves>(a, c.e, c0, wave, r0, c.n, tok, sx, sw, stage, acc);
+  gate_up_sums<MF, FC, PF, WK>(a, c.e, c0, part, r0, c.n, tok, sx, sw, stage, acc);
   __syncthreads();   // the scales' place is free
-  v4f* red = reinterpret_cast<v4f*>(lds);
-  if (wave > 0) {
+  if constexpr (WK > 1) {
+    v4f* red = reinterpret_cast<v4f*>(lds) + tile * (WK - 1) * 2 * FC * MF * 64;
+    if (part > 0) {
 #pragma unroll
-    for (int f = 0; f < 2 * FC; ++f)
+      for (int f = 0; f < 2 * FC; ++f)
 #pragma unroll
-      for (int j = 0; j < MF; ++j) red[(((wave - 1) * 2 * FC + f) * MF + j) * 64 + lane] = acc[f][j];
+        for (int j = 0; j < MF; ++j) red[(((part - 1) * 2 * FC + f) * MF + j) * 64 + lane] = acc[f][j];
+    }
+    __syncthreads();
+    if (part == 0) {
+#pragma unroll
+      for (int w = 0; w < WK - 1; ++w)
+#pragma unroll
+        for (int f = 0; f < 2 * FC; ++f)
+#pragma unroll
+          for (int j = 0; j < MF; ++j) acc[f][j] += red[((w * 2 * FC + f) * MF + j) * 64 + lane];
+    }
   }
-  __syncthreads();
-  if (wave == 0) {
+  if (part == 0) {
 #pragma unroll
     for (int j = 0; j < MF; ++j) {
-#pragma unroll
-      for (int w = 0; w < kGuWaves - 1; ++w)
-#pragma unroll
-        for (int f = 0; f < 2 * FC; ++f) acc[f][j] += red[((w * 2 * FC + f) * MF + j) * 64 + lane];
       const int r = r0 + 16 * j + (lane & 15);
 #pragma unroll
       for (int f = 0; f < FC; ++f)
@@ -341,20 +350,20 @@ __device__ __forceinline__ void gate_up_rows(const MoeArgs& a, const Chosen& c, 
               silu_mul(acc[f][j], acc[FC + f][j]);
     }
   }
-  __syncthreads();
+  if (r0 + 16 * MF < c.n) __syncthreads();
 }
 
 // MFBIG: fragments of rows at a time for an expert of more than 16 rows.
-template <int MFBIG, int FC>
-__global__ __launch_bounds__(kGuThreads, 4) void k_moe_gate_up(MoeArgs a) {
+template <int MFBIG, int FC, int WK>
+__global__ __launch_bounds__(kGuThreads, MFBIG == 4 ? 3 : 4) void k_moe_gate_up(MoeArgs a) {
   __shared__ uint16_t tok[kMaxPairs];
   extern __shared__ float lds[];   // E ints, then the scales, then the waves' sums
   const Chosen c = choose(a, blockIdx.y, blockIdx.x == 0, reinterpret_cast<int*>(lds), tok);
   if (c.e < 0) return;
   if (c.n <= 16) {
-    gate_up_rows<1, FC, FC == 1 ? 4 : 2>(a, c, 0, tok, lds);
+    gate_up_rows<1, FC, FC == 1 ? 4 : 2, WK>(a, c, 0, tok, lds);
   } else {
-    for (int r0 = 0; r0 < c.n; r0 += 16 * MFBIG) gate_up_rows<MFBIG, FC, 1>(a, c, r0, tok, lds);
+    for (int r0 = 0; r0 < c.n; r0 += 16 * MFBIG) gate_up_rows<MFBIG, FC, 1, WK>(a, c, r0, tok, lds);
   }
 }
 
@@ -394,6 +403,9 @@ constexpr int kDownWaves = 8, kDownThreads = 64 * kDownWaves;
 
 // Pairs whose h every down workgroup quantises for itself, at most.
 constexpr int64_t kLdsPairs = 64, kLdsCodes = 32768;
+
+// Up to this K the experts may be split over workgroups.
+constexpr int64_t kSplitMaxK = 4096;
 
 // LDSH (few pairs): every workgroup quantises the h of all pairs into LDS
 // (rows of I + 16 bytes, so that the 16 rows of a fragment read lie in
@@ -507,8 +519,11 @@ __global__ __launch_bounds__(kDownThreads, 2) void k_moe_down(MoeArgs a, int cw,
   };
 
   const int G = (IB + smax - 1) / smax, per = (IB + G - 1) / G;   // blocks per granule, granules per unit
-  const int lo = (int)((int64_t)units * per * wave / kDownWaves);
-  const int hi = (int)((int64_t)units * per * (wave + 1) / kDownWaves);
+  // this workgroup's units, of all the workgroups of its columns
+  const int u_lo = (int)((int64_t)units * blockIdx.y / gridDim.y);
+  const int u_n = (int)((int64_t)units * (blockIdx.y + 1) / gridDim.y) - u_lo;
+  const int lo = u_lo * per + (int)((int64_t)u_n * per * wave / kDownWaves);
+  const int hi = u_lo * per + (int)((int64_t)u_n * per * (wave + 1) / kDownWaves);
   // blocks before granule g, counted over the units in a row
   auto blocks_before = [&](int g) { return g / per * IB + (g % per) * G; };
   const int todo = blocks_before(hi) - blocks_before(lo);
@@ -652,6 +667,18 @@ __global__ __launch_bounds__(kDownThreads, 2) void k_moe_down(MoeArgs a, int cw,
     }
   }
   __syncthreads();
+  if (gridDim.y > 1) {   // k_moe_combine sums the pairs
+    for (int k = wave; k < u_n; k += kDownWaves) {
+      const Unit c = unit(u_lo + k);
+      for (int i = lane; i < c.rows * cols; i += 64) {
+        const int r = i / cols, col = i - r * cols;
+        float o = lds[(c.base + r) * 16 * FN + col];
+        for (int s = 1; s < smax; ++s) o += lds[(s * P + c.base + r) * 16 * FN + col];
+        a.out32[(int64_t)(c.base + r) * a.K + n0 + col] = o;
+      }
+    }
+    return;
+  }
   for (int i = threadIdx.x; i < a.T * cols; i += kDownThreads) {
     const int t = i / cols, col = i - t * cols;
     float y = 0.f;
@@ -672,22 +699,64 @@ __global__ __launch_bounds__(kDownThreads, 2) void k_moe_down(MoeArgs a, int cw,
 
 bool quant_in_down(int64_t P, int64_t I) { return P <= kLdsPairs && P * I <= kLdsCodes; }
 
-// Columns per down workgroup: a multiple of 4 up to 32, the widest of those
-// that give the fullest CU the fewest columns.
-int down_columns(int K) {
-  int best = 16, most = 1 << 30;
-  for (int cw = 32; cw >= 4; cw -= 4) {
-    const int wgs = (K + cw - 1) / cw, load = (wgs + 255) / 256 * cw;
-    if (load < most) {
-      most = load;
-      best = cw;
-    }
+// Y from the pairs' products, 4 columns per thread, in slot order.
+template <int OUT>
+__global__ __launch_bounds__(256) void k_moe_combine(MoeArgs a) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.T * (a.K >> 2)) return;
+  const int t = i / (a.K >> 2), n = (i - t * (a.K >> 2)) * 4;
+  float y[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < a.topk; ++j) {
+    const int p = t * a.topk + j, r = a.pos[p];
+    if (r < 0) continue;
+    const float4 o = *reinterpret_cast<const float4*>(a.out32 + (int64_t)r * a.K + n);
+    const float w = a.weights[p];
+    y[0] = __builtin_fmaf(w, o.x, y[0]);
+    y[1] = __builtin_fmaf(w, o.y, y[1]);
+    y[2] = __builtin_fmaf(w, o.z, y[2]);
+    y[3] = __builtin_fmaf(w, o.w, y[3]);
   }
+  const int64_t at = (int64_t)t * a.K + n;
+  if (OUT == OUT_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(a.Y) + at) = make_float4(y[0], y[1], y[2], y[3]);
+  } else {
+    uint2 o;
+    o.x = f32_to_bf16_rne(y[0]) | (f32_to_bf16_rne(y[1]) << 16);
+    o.y = f32_to_bf16_rne(y[2]) | (f32_to_bf16_rne(y[3]) << 16);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.Y) + at) = o;
+  }
+}
+
+// The down kernel's grid: columns per workgroup and workgroups per columns.
+struct DownGrid {
+  int cw, z;
+};
+
+// The fullest CU's time: its workgroups' blocks times the 128-byte lines of a
+// block (a weight row each, a row of h each, the scales) at about 4.5 ns a
+// line, and 6 us for the combine kernel where the experts are split over
+// workgroups (z > 1: few columns, many pairs; a workgroup of few columns loads
+// more of h than of the weights).  K = 256, I = 2816, 24 experts, 84 pairs:
+// 64 workgroups of 4 columns 24 us, 256 of 16 columns and a sixteenth of the
+// experts 5 us and the combine.
+DownGrid down_grid(int64_t P, int64_t most, int64_t K, int64_t IB, bool in_down) {
+  DownGrid best{16, 1};
+  double best_t = 1e30;
+  for (int z = 1; z <= (in_down || K > kSplitMaxK ? 1 : 16); z *= 2)
+    for (int cw = 32; cw >= 4; cw -= 4) {
+      const int64_t wgs = (K + cw - 1) / cw * z, blocks = (most + z - 1) / z * IB;
+      const double lines = cw + 2 + (in_down ? 0.0 : (double)P / most);
+      const double t = (double)((wgs + 255) / 256) * blocks * lines * 4.5e-3 + (z > 1 ? 6.0 : 0.0);
+      if (t < best_t) {
+        best_t = t;
+        best = {cw, z};
+      }
+    }
   return best;
 }
 
 template <int MF, int FN, int PF, bool LDSH>
-hipError_t down_launch(const MoeArgs& a, OutKind out, int cw, int most, hipStream_t st) {
+hipError_t down_launch(const MoeArgs& a, OutKind out, DownGrid g, int most, hipStream_t st) {
   const int P = a.T * a.topk, IB = a.I / 128;
   const size_t res = (size_t)P * FN * 64;
   const size_t rest = (size_t)(P * 14 + 15) / 16 * 16 +
@@ -696,23 +765,24 @@ hipError_t down_launch(const MoeArgs& a, OutKind out, int cw, int most, hipStrea
   const int cuts = 4 * P >= kDownWaves ? 4 : kDownWaves;
   int smax = 1;
   while (smax * 2 <= IB && smax * 2 <= cuts && smax * 2 * res + rest <= 131072) smax *= 2;
-  const dim3 grid((unsigned)((a.K + cw - 1) / cw)), block(kDownThreads);
+  const dim3 grid((unsigned)((a.K + g.cw - 1) / g.cw), (unsigned)g.z), block(kDownThreads);
   const size_t lds = smax * res + rest;
   if (out == OUT_F32)
-    hipLaunchKernelGGL((k_moe_down<MF, FN, PF, OUT_F32, LDSH>), grid, block, lds, st, a, cw, smax, most);
+    hipLaunchKernelGGL((k_moe_down<MF, FN, PF, OUT_F32, LDSH>), grid, block, lds, st, a, g.cw, smax, most);
   else
-    hipLaunchKernelGGL((k_moe_down<MF, FN, PF, OUT_BF16, LDSH>), grid, block, lds, st, a, cw, smax, most);
+    hipLaunchKernelGGL((k_moe_down<MF, FN, PF, OUT_BF16, LDSH>), grid, block, lds, st, a, g.cw, smax, most);
   return hipGetLastError();
 }
 
-template <int MFBIG, int FC>
+template <int MFBIG, int FC, int WK>
 hipError_t gate_up_launch(const MoeArgs& a, int most, hipStream_t st) {
   const int KB = a.K >> 7;
-  const size_t sums = (size_t)(kGuWaves - 1) * 2 * FC * MFBIG * 1024, owner = (size_t)a.E * 4;
+  const size_t sums = (size_t)(kGuWaves / WK) * (WK - 1) * 2 * FC * MFBIG * 1024, owner = (size_t)a.E * 4;
   const size_t scales = ((size_t)2 * KB + (size_t)16 * MFBIG * (KB | 1)) * 4;
   size_t lds = sums > owner ? sums : owner;
   if (scales > lds) lds = scales;
-  hipLaunchKernelGGL((k_moe_gate_up<MFBIG, FC>), dim3((unsigned)(a.I / (16 * FC)), (unsigned)most), dim3(kGuThreads),
+  const int cols = 16 * FC * (kGuWaves / WK);
+  hipLaunchKernelGGL((k_moe_gate_up<MFBIG, FC, WK>), dim3((unsigned)(a.I / cols), (unsigned)most), dim3(kGuThreads),
                      lds, st, a);
   return hipGetLastError();
 }
@@ -720,8 +790,9 @@ hipError_t gate_up_launch(const MoeArgs& a, int most, hipStream_t st) {
 }  // namespace
 
 // Workspace: h (fp32), its codes and their scales, a row per pair; each
-// pair's row; the chosen experts' indices, rows and first rows.
-int64_t moe_workspace(int64_t T, int64_t topk, int64_t I, MoeArgs* a, void* ws) {
+// pair's row; the chosen experts' indices, rows and first rows; the pairs'
+// products where several workgroups share the columns.
+int64_t moe_workspace(int64_t T, int64_t topk, int64_t I, int64_t K, MoeArgs* a, void* ws) {
   const int64_t P = T * topk;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -738,6 +809,7 @@ int64_t moe_workspace(int64_t T, int64_t topk, int64_t I, MoeArgs* a, void* ws) 
   m.expert = reinterpret_cast<int32_t*>(take(P * 4));
   m.count = reinterpret_cast<int32_t*>(take(P * 4));
   m.start = reinterpret_cast<int32_t*>(take(P * 4));
+  m.out32 = reinterpret_cast<float*>(take(in_down || K > kSplitMaxK ? 0 : P * K * 4));
   if (a) *a = m;
   return at;
 }
@@ -745,25 +817,39 @@ int64_t moe_workspace(int64_t T, int64_t topk, int64_t I, MoeArgs* a, void* ws) 
 hipError_t launch_moe_block(const MoeArgs& a, OutKind out, hipStream_t st) {
   const int P = a.T * a.topk, IB = a.I / 128;
   const int most = P < a.E ? P : a.E;   // chosen experts, at most
-  const bool wide = (int64_t)(a.I / 32) * most >= 256;
-  hipError_t e = P > 12 * a.E ? gate_up_launch<4, 1>(a, most, st)
-                 : wide       ? gate_up_launch<2, 2>(a, most, st)
-                              : gate_up_launch<2, 1>(a, most, st);
+  // columns per gate_up workgroup: 32 load the activations half as often as
+  // 16, which spread few columns more evenly (one token of 8 experts,
+  // K = 7168, I = 2048: 43 us with 32, 45 with 16; 7 experts, I = 256: 21 and
+  // 16); 64, with half the waves per column, for short K, where a workgroup's
+  // start is most of its time (K = 256, 24 experts, I = 2816: 13 us, 17, 27)
+  const int64_t w16 = (int64_t)(a.I / 16) * most, w32 = w16 / 2;
+  const bool narrow = 5 * ((w16 + 255) / 256) * 16 < 4 * ((w32 + 255) / 256) * 32;
+  hipError_t e = P > 12 * a.E                                ? gate_up_launch<4, 1, 4>(a, most, st)
+                 : a.K <= 1024 && w16 / 4 >= 512             ? gate_up_launch<2, 2, 2>(a, most, st)
+                 : narrow                                    ? gate_up_launch<2, 1, 4>(a, most, st)
+                                                             : gate_up_launch<2, 2, 4>(a, most, st);
   if (e != hipSuccess) return e;
-  const int cw = down_columns(a.K);
-  if (quant_in_down(P, a.I))
-    return cw <= 16 ? down_launch<1, 1, 8, true>(a, out, cw, most, st)
-                    : down_launch<1, 2, 6, true>(a, out, cw, most, st);
+  const bool in_down = quant_in_down(P, a.I);
+  const DownGrid g = down_grid(P, most, a.K, IB, in_down);
+  const bool one = g.cw <= 16;   // one fragment of columns
+  if (in_down)
+    return one ? down_launch<1, 1, 8, true>(a, out, g, most, st) : down_launch<1, 2, 6, true>(a, out, g, most, st);
   hipLaunchKernelGGL(k_moe_quant, dim3((unsigned)((P * IB + 31) / 32)), dim3(256), 0, st, a, P, IB);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   // rows per unit by the mean rows of an expert (a unit of more rows than its
   // expert has costs registers, one of fewer reads the weights again)
   if (P <= 12 * a.E)
-    return cw <= 16 ? down_launch<1, 1, 8, false>(a, out, cw, most, st)
-                    : down_launch<1, 2, 6, false>(a, out, cw, most, st);
-  return cw <= 16 ? down_launch<4, 1, 3, false>(a, out, cw, most, st)
-                  : down_launch<4, 2, 3, false>(a, out, cw, most, st);
+    e = one ? down_launch<1, 1, 8, false>(a, out, g, most, st) : down_launch<1, 2, 6, false>(a, out, g, most, st);
+  else
+    e = one ? down_launch<4, 1, 3, false>(a, out, g, most, st) : down_launch<4, 2, 3, false>(a, out, g, most, st);
+  if (e != hipSuccess || g.z == 1) return e;
+  const dim3 grid((unsigned)(((int64_t)a.T * (a.K / 4) + 255) / 256));
+  if (out == OUT_F32)
+    hipLaunchKernelGGL((k_moe_combine<OUT_F32>), grid, dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_moe_combine<OUT_BF16>), grid, dim3(256), 0, st, a);
+  return hipGetLastError();
 }
 
 }  // namespace w8
