@@ -355,7 +355,7 @@ __device__ __forceinline__ void gate_up_rows(const MoeArgs& a, const Chosen& c, 
 
 // MFBIG: fragments of rows at a time for an expert of more than 16 rows.
 template <int MFBIG, int FC, int WK>
-__global__ __launch_bounds__(kGuThreads, MFBIG == 4 ? 3 : 4) void k_moe_gate_up(MoeArgs a) {
+__global__ __launch_bounds__(kGuThreads, MFBIG == 4 ? 2 : 4) void k_moe_gate_up(MoeArgs a) {
   __shared__ uint16_t tok[kMaxPairs];
   extern __shared__ float lds[];   // E ints, then the scales, then the waves' sums
   const Chosen c = choose(a, blockIdx.y, blockIdx.x == 0, reinterpret_cast<int*>(lds), tok);
@@ -824,7 +824,7 @@ hipError_t launch_moe_block(const MoeArgs& a, OutKind out, hipStream_t st) {
   // start is most of its time (K = 256, 24 experts, I = 2816: 13 us, 17, 27)
   const int64_t w16 = (int64_t)(a.I / 16) * most, w32 = w16 / 2;
   const bool narrow = 5 * ((w16 + 255) / 256) * 16 < 4 * ((w32 + 255) / 256) * 32;
-  hipError_t e = P > 12 * a.E                                ? gate_up_launch<4, 1, 4>(a, most, st)
+  hipError_t e = P > 24 * a.E                                ? gate_up_launch<4, 2, 4>(a, most, st)
                  : a.K <= 1024 && w16 / 4 >= 512             ? gate_up_launch<2, 2, 2>(a, most, st)
                  : narrow                                    ? gate_up_launch<2, 1, 4>(a, most, st)
                                                              : gate_up_launch<2, 2, 4>(a, most, st);
@@ -841,6 +841,8 @@ hipError_t launch_moe_block(const MoeArgs& a, OutKind out, hipStream_t st) {
   // expert has costs registers, one of fewer reads the weights again)
   if (P <= 12 * a.E)
     e = one ? down_launch<1, 1, 8, false>(a, out, g, most, st) : down_launch<1, 2, 6, false>(a, out, g, most, st);
+  else if (P <= 28 * a.E)
+    e = one ? down_launch<2, 1, 6, false>(a, out, g, most, st) : down_launch<2, 2, 4, false>(a, out, g, most, st);
   else
     e = one ? down_launch<4, 1, 3, false>(a, out, g, most, st) : down_launch<4, 2, 3, false>(a, out, g, most, st);
   if (e != hipSuccess || g.z == 1) return e;
