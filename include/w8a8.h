@@ -438,9 +438,9 @@ int norm_residual_quant(const void* y, const void* residual, const void* post_we
 enum w8_route_score { W8_ROUTE_SOFTMAX = 0, W8_ROUTE_SIGMOID = 1 };
 
 int moe_route_topk(const void* logits, int logits_dtype, const float* bias,
-                   int score, int64_t T, int64_t E, int topk, int n_group,
-                   int topk_group, int group_top, int renormalise, double scale,
-                   int32_t* ids, float* weights, void* stream);
+                   int score, int64_t T, int64_t E, int64_t topk, int64_t n_group,
+                   int64_t topk_group, int64_t group_top, int renormalise,
+                   double scale, int32_t* ids, float* weights, void* stream);
 
 /*
  * A whole mixture-of-experts layer for a few tokens (up to 64; for more,

@@ -141,6 +141,18 @@ def test_norm_in_place_and_out():
         assert all(bool((b[37] == 9).all()) for b in bufs)
 
 
+def test_norm_more_rows_than_a_launch_takes():
+    """2^20 + 3 rows: two launches, the second of three rows."""
+    M, K = (1 << 20) + 3, 128
+    y = torch.randn(M, K, device=DEV).to(torch.bfloat16)
+    w = torch.ones(K, device=DEV, dtype=torch.bfloat16)
+    g = torch.randn(M, K, device=DEV).to(torch.bfloat16)
+    got = w8.norm_residual_quant(y, w, residual=y, gate=g, normed=True)
+    for part in (slice(0, 5), slice((1 << 20) - 3, M)):
+        assert _same(w8.norm_residual_quant(y[part], w, residual=y[part], gate=g[part], normed=True),
+                     [t[part] for t in got])
+
+
 def test_norm_refusals():
     d = {k: v.to(DEV) for k, v in _norm_inputs(4, 256, torch.bfloat16, seed=8).items()}
     bad = [dict(residual=d["residual"][:3]), dict(residual=d["residual"].half()), dict(gate=d["gate"][:2]),
@@ -279,7 +291,8 @@ def _to(args):
     (1, 1, 1, 128, 128), (1, 2, 4, 256, 384), (1, 8, 16, 128, 1024), (2, 3, 5, 384, 256), (3, 16, 20, 128, 128),
     (5, 2, 3, 640, 256), (7, 6, 8, 256, 640), (16, 2, 4, 128, 256), (17, 4, 4, 256, 128), (20, 1, 1, 128, 256),
     (32, 3, 6, 128, 384), (33, 2, 2, 256, 256), (48, 1, 1, 384, 128), (64, 8, 12, 128, 256), (64, 1, 1, 256, 128),
-    (64, 16, 40, 128, 128), (40, 5, 24, 384, 1280), (64, 2, 3, 1024, 384), (33, 8, 64, 128, 2176), (1, 1, 300, 128, 128), (4, 2, 8, 1152, 128), (3, 1, 2, 128, 2176)])
+    (64, 16, 40, 128, 128), (40, 5, 24, 384, 1280), (64, 2, 3, 1024, 384), (33, 8, 64, 128, 2176), (2, 2, 2, 128, 32768),
+    (2, 2, 2, 32768, 128), (64, 1, 1, 128, 32768), (64, 2, 2, 1024, 4096), (40, 4, 5, 512, 384), (1, 1, 300, 128, 128), (4, 2, 8, 1152, 128), (3, 1, 2, 128, 2176)])
 def test_moe(T, topk, E, I, K):
     print(f"moe T={T} topk={topk} E={E} I={I} K={K}", flush=True)
     args = _moe_inputs(T, topk, E, I, K, seed=T + E + I)

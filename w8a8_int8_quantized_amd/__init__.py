@@ -94,8 +94,8 @@ _FUNCS = {
                                                                    ctypes.c_float, ctypes.c_int, ctypes.c_int,
                                                                    ctypes.c_int64, ctypes.c_int64]
                             + [ctypes.c_void_p] * 5),
-    "moe_route_topk": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
-                                      ctypes.c_int64] + [ctypes.c_int] * 5 + [ctypes.c_double] + [ctypes.c_void_p] * 3),
+    "moe_route_topk": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_int]
+                       + [ctypes.c_int64] * 6 + [ctypes.c_int, ctypes.c_double] + [ctypes.c_void_p] * 3),
     "moe_workspace_bytes": (ctypes.c_int64, [ctypes.c_int64] * 4),
     "moe_w8a8_block": (ctypes.c_int, [ctypes.c_void_p] * 9 + [ctypes.c_int] + [ctypes.c_int64] * 5
                        + [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
@@ -434,6 +434,11 @@ def _like(t, name, shape, dtype, dev):
         raise W8Error(f"{name} must be contiguous")
 
 
+def _dims(t, name, n):
+    if t.dim() != n:
+        raise W8Error(f"{name} must have {n} dimensions, got {tuple(t.shape)}")
+
+
 def _run_on(dev, what, fn, *args):
     """The call on dev's current stream, with dev the current device."""
     if dev.index == torch.cuda.current_device():
@@ -463,6 +468,7 @@ def norm_residual_quant(y, pre_weight, residual=None, post_weight=None, gate=Non
     order; h may be residual or y itself.
     """
     _dev(y)
+    _dims(y, "y", 2)
     M, K = y.shape
     dev, dt, code = y.device, y.dtype, _act_dtype(y)
     if scheme not in (W8_SCHEME_BLOCK, W8_SCHEME_CHANNEL, None):
@@ -512,6 +518,7 @@ def moe_route_topk(logits, topk, bias=None, score=W8_ROUTE_SOFTMAX, n_group=1, t
     and weight 0.
     """
     _dev(logits)
+    _dims(logits, "logits", 2)
     T, E = logits.shape
     dev = logits.device
     code = W8_FP32 if logits.dtype == torch.float32 else _act_dtype(logits)
@@ -552,6 +559,9 @@ def moe_w8a8_block(A, a_scale, topk_ids, topk_weights, W_gate_up, gate_up_scale,
     topk, I, K) or more; without one, torch allocates it for the call.
     """
     _dev(A)
+    _dims(A, "A", 2)
+    _dims(topk_ids, "topk_ids", 2)
+    _dims(W_gate_up, "W_gate_up", 3)
     T, K = A.shape
     E, I2, _ = W_gate_up.shape
     topk, I, dev = topk_ids.shape[1], I2 // 2, A.device

@@ -393,8 +393,8 @@ int norm_residual_quant(const void* y, const void* residual, const void* post_we
 }
 
 int moe_route_topk(const void* logits, int logits_dtype, const float* bias, int score, int64_t T, int64_t E,
-                   int topk, int n_group, int topk_group, int group_top, int renormalise, double scale, int32_t* ids,
-                   float* weights, void* stream) {
+                   int64_t topk, int64_t n_group, int64_t topk_group, int64_t group_top, int renormalise, double scale,
+                   int32_t* ids, float* weights, void* stream) {
   if (logits_dtype != W8_BF16 && logits_dtype != W8_FP16 && logits_dtype != W8_FP32) return W8_ERR_DTYPE;
   if (score != W8_ROUTE_SOFTMAX && score != W8_ROUTE_SIGMOID) return W8_ERR_DTYPE;
   if (T < 0 || T > kMaxRows || E < 1 || E > w8::kRouteMaxE || topk < 1 || topk > w8::kRouteMaxTopk)
@@ -415,10 +415,10 @@ int moe_route_topk(const void* logits, int logits_dtype, const float* bias, int 
   a.weights = weights;
   a.scale = scale;
   a.E = (int)E;
-  a.topk = topk;
-  a.n_group = n_group;
-  a.topk_group = topk_group;
-  a.group_top = group_top;
+  a.topk = (int)topk;
+  a.n_group = (int)n_group;
+  a.topk_group = (int)topk_group;
+  a.group_top = (int)group_top;
   a.dtype = logits_dtype;
   a.sigmoid = score == W8_ROUTE_SIGMOID;
   a.renormalise = renormalise != 0;

@@ -73,6 +73,7 @@ struct NormArgs {
   int8_t* q;
   float* q_scale;
   int64_t gate_rows;   // 1 or M
+  int64_t row0;        // set by the launcher: the launch's first row
   int K;
   float residual_scale, eps;
   bool group;          // the quantiser's granularity: 1 x 128, or a row
@@ -89,6 +90,7 @@ struct RouteArgs {
   double scale;
   int E, topk, n_group, topk_group, group_top, dtype;   // dtype: a w8_dtype
   bool sigmoid, renormalise;
+  int64_t t0;           // set by the launcher: the launch's first token
   uint32_t per_magic;   // set by the launcher: e / (E / n_group) = e * per_magic >> 20
 };
 hipError_t launch_route_topk(RouteArgs a, int64_t T, hipStream_t st);

@@ -96,7 +96,7 @@ template <bool FP16, int NT, int CH, bool LATE>
 __global__ __launch_bounds__(NT, LATE ? 8 : 1) void k_norm_residual_quant(NormArgs a) {
   constexpr int NW = NT / 64;
   __shared__ float red[3][NW];
-  const int64_t row = blockIdx.x;
+  const int64_t row = a.row0 + blockIdx.x;
   const int nch = a.K >> 3;
   const Row y(a.y, row, a.K), res(a.residual, row, a.K), gate(a.gate, a.gate_rows == 1 ? 0 : row, a.K),
       pw(a.post_weight, 0, a.K), nw(a.pre_weight, 0, a.K);
@@ -192,10 +192,17 @@ __global__ __launch_bounds__(NT, LATE ? 8 : 1) void k_norm_residual_quant(NormAr
   if (!group && threadIdx.x == 0) a.q_scale[row] = make_scale(amax).s;
 }
 
+// A launch holds fewer than 2^32 threads: rows in parts of 2^20.
 template <bool FP16, int NT, int CH, bool LATE = false>
-hipError_t norm_go(const NormArgs& a, int64_t M, hipStream_t st) {
-  hipLaunchKernelGGL((k_norm_residual_quant<FP16, NT, CH, LATE>), dim3((unsigned)M), dim3(NT), 0, st, a);
-  return hipGetLastError();
+hipError_t norm_go(NormArgs a, int64_t M, hipStream_t st) {
+  constexpr int64_t kPart = int64_t(1) << 20;
+  for (a.row0 = 0; a.row0 < M; a.row0 += kPart) {
+    const int64_t n = M - a.row0 < kPart ? M - a.row0 : kPart;
+    hipLaunchKernelGGL((k_norm_residual_quant<FP16, NT, CH, LATE>), dim3((unsigned)n), dim3(NT), 0, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // Few rows leave CUs idle: the row is spread as thin as it goes.  With more

@@ -48,7 +48,7 @@ template <int NE>
 __global__ __launch_bounds__(64) void k_route_topk(RouteArgs a) {
   extern __shared__ double lds[];
   const int E = a.E, lane = threadIdx.x;
-  const int64_t t = blockIdx.x;
+  const int64_t t = a.t0 + blockIdx.x;
   double* lc = lds;
   double* lw = lc + E;
   double* gs = lw + E;
@@ -206,10 +206,16 @@ __global__ __launch_bounds__(64) void k_route_topk(RouteArgs a) {
 }
 
 template <int NE>
-hipError_t route_launch(const RouteArgs& a, int64_t T, hipStream_t st) {
+hipError_t route_launch(RouteArgs a, int64_t T, hipStream_t st) {
   const size_t lds = (size_t)a.E * 16 + (a.n_group > 1 ? (size_t)a.n_group * 9 : 0);
-  hipLaunchKernelGGL((k_route_topk<NE>), dim3((unsigned)T), dim3(64), lds, st, a);
-  return hipGetLastError();
+  constexpr int64_t kPart = int64_t(1) << 24;   // a launch holds fewer than 2^32 threads
+  for (a.t0 = 0; a.t0 < T; a.t0 += kPart) {
+    const int64_t n = T - a.t0 < kPart ? T - a.t0 : kPart;
+    hipLaunchKernelGGL((k_route_topk<NE>), dim3((unsigned)n), dim3(64), lds, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
