@@ -426,12 +426,13 @@ def gemm_w8a8_asym(A, a_params, W, w_scale, w_sum, out_dtype=torch.bfloat16, out
 # --------------------------------------------- the layer around the products
 def _like(t, name, shape, dtype, dev):
     """t is a contiguous tensor of this shape (a tuple) and type on dev."""
+    if t.shape == shape and t.dtype == dtype and t.device == dev and t.is_contiguous():
+        return
     if t.dtype != dtype or t.shape != shape:
         raise W8Error(f"{name} must be {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
     if t.device != dev:
         raise W8Error(f"{name} must be on {dev}")
-    if not t.is_contiguous():
-        raise W8Error(f"{name} must be contiguous")
+    raise W8Error(f"{name} must be contiguous")
 
 
 def _dims(t, name, n):
@@ -484,20 +485,23 @@ def norm_residual_quant(y, pre_weight, residual=None, post_weight=None, gate=Non
     if gate is not None:
         gate_rows = 1 if gate.dim() == 1 else M
         _like(gate, "gate", (K,) if gate.dim() == 1 else (M, K), dt, dev)
-    want = [("h", (M, K), dt)]
-    if scheme is not None:
-        want += [("q", (M, K), torch.int8), ("scales", (M, K // GROUP) if scheme == W8_SCHEME_BLOCK else (M,),
-                                             torch.float32)]
-    if normed:
-        want += [("z", (M, K), dt)]
+    sshape = (M, K // GROUP) if scheme == W8_SCHEME_BLOCK else (M,)
     if out is None:
-        out = tuple(torch.empty(shape, dtype=t, device=dev) for _, shape, t in want)
+        out = (torch.empty_like(y),)
+        if scheme is not None:
+            out += (torch.empty_like(y, dtype=torch.int8), torch.empty(sshape, dtype=torch.float32, device=dev))
+        if normed:
+            out += (torch.empty_like(y),)
     else:
         out = tuple(out)
-        if len(out) != len(want):
-            raise W8Error(f"norm_residual_quant: out must be ({', '.join(n for n, _, _ in want)})")
-        for t, (name, shape, ty) in zip(out, want):
-            _like(t, "out " + name, shape, ty, dev)
+        names = ("h",) + (("q", "scales") if scheme is not None else ()) + (("z",) if normed else ())
+        if len(out) != len(names):
+            raise W8Error(f"norm_residual_quant: out must be ({', '.join(names)})")
+        for t, name in zip(out, names):
+            if name == "scales":
+                _like(t, "out scales", sshape, torch.float32, dev)
+            else:
+                _like(t, "out " + name, (M, K), torch.int8 if name == "q" else dt, dev)
     q, s = (out[1], out[2]) if scheme is not None else (None, None)
     _run_on(dev, "norm_residual_quant", lib.norm_residual_quant, y.data_ptr(), _ptr(residual), _ptr(post_weight),
             _ptr(gate), gate_rows, residual_scale, pre_weight.data_ptr(), eps, code, scheme or 0, M, K,
@@ -585,6 +589,6 @@ def moe_w8a8_block(A, a_scale, topk_ids, topk_weights, W_gate_up, gate_up_scale,
         raise W8Error(f"workspace must be contiguous, on {dev}")
     _run_on(dev, "moe_w8a8_block", lib.moe_w8a8_block, A.data_ptr(), a_scale.data_ptr(), topk_ids.data_ptr(),
             topk_weights.data_ptr(), W_gate_up.data_ptr(), gate_up_scale.data_ptr(), W_down.data_ptr(),
-            down_scale.data_ptr(), out.data_ptr(), _out_code(out.dtype), T, topk, E, I, K, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
+            down_scale.data_ptr(), out.data_ptr(), W8_FP32 if out.dtype == torch.float32 else W8_BF16, T, topk, E, I,
+            K, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
