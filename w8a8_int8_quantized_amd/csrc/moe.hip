@@ -1,4 +1,4 @@
-// A whole mixture-of-experts layer for a few tokens, in two kernels (gfx950).
+// A whole mixture-of-experts layer for a few tokens (gfx950).
 //
 //   gate, up = blockwise(A[t], W_gate_up[e])         exact int32 per 128 of K
 //   hq, hs   = group quantiser of silu(gate) * up    fp32, groups of 128
@@ -10,9 +10,14 @@
 // DeepSeek", section 1.2.
 //
 // With at most 64 tokens the experts' weights are nearly all of the traffic
-// (3 I K bytes for each expert that a token chose), so both kernels stream
-// them once, straight from global memory into MFMA operand registers.  A
-// "pair" is one slot of one token (t, j), p = t topk + j; the pairs of one
+// (3 I K bytes for each expert that a token chose), so two kernels stream
+// them once, straight from global memory into MFMA operand registers:
+// k_moe_gate_up and k_moe_down.  Between them h is quantised, by the down
+// kernel itself where the pairs are few, else by k_moe_quant; where the output
+// has few columns, k_moe_combine sums what several down workgroups share.
+// 64 tokens, K = 7168, I = 2048, 64 experts, 8 of them per token (2.8 GB of
+// weights, each byte fetched once by the counters): 314 + 5 + 163 us, 6.0 and
+// 5.8 TB/s; one token (352 MB): 43 + 27 us.  A "pair" is one slot of one token (t, j), p = t topk + j; the pairs of one
 // expert are the rows of its products, in the order of p, and the rows of all
 // experts in the order of the expert index are the rows of hq.  A pair whose
 // id is outside 0 .. E - 1 has no row.
@@ -146,7 +151,15 @@ __device__ __forceinline__ v4f silu_mul(v4f g, v4f u) {
 
 // The group quantiser of 16 of a group's values per lane, 8 lanes per group.
 // h is quantised from fp32 (a 16-bit h would be read by nobody).
-__device__ __forceinline__ uint4 quant16(float* v, float* scale) {
+__device__ __forceinline__ uint4 quant16(const float4* raw, float* scale) {
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[4 * i] = raw[i].x;
+    v[4 * i + 1] = raw[i].y;
+    v[4 * i + 2] = raw[i].z;
+    v[4 * i + 3] = raw[i].w;
+  }
   const QScale sc = make_scale(max8(amax_n(v, 16)));
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = quant_one(v[i], sc);
@@ -271,8 +284,10 @@ __device__ __forceinline__ Chosen choose(const MoeArgs& a, int k, bool table, in
 // split 16 FC 4 / WK columns of h of one expert, WK of them sharing 16 FC
 // columns and splitting the K blocks.  A workgroup this small keeps the load
 // of the CUs even: each CU streams at a rate of its own (its outstanding
-// loads over the memory's latency), so the kernel takes as long as the CU
-// with the most to load.  The 128 columns of a quantisation group may lie in
+// loads over the memory's latency, some 23 GB/s when all are at it), so the
+// kernel takes as long as the CU with the most to load (128-column
+// workgroups, one pass more than their number filled, 138 us where these take
+// 102: 8 tokens, K = 4096, I = 1536).  The 128 columns of a quantisation group may lie in
 // several workgroups; h leaves in fp32 and is quantised by its readers.
 template <int MF, int FC, int PF, int WK>
 __device__ __forceinline__ void gate_up_rows(const MoeArgs& a, const Chosen& c, int r0, const uint16_t* tok,
@@ -357,7 +372,7 @@ __device__ __forceinline__ void gate_up_rows(const MoeArgs& a, const Chosen& c, 
 template <int MFBIG, int FC, int WK>
 __global__ __launch_bounds__(kGuThreads, MFBIG == 4 ? 2 : 4) void k_moe_gate_up(MoeArgs a) {
   __shared__ uint16_t tok[kMaxPairs];
-  extern __shared__ float lds[];   // E ints, then the scales, then the waves' sums
+  extern __shared__ __align__(16) float lds[];   // E ints, then the scales, then the waves' sums
   const Chosen c = choose(a, blockIdx.y, blockIdx.x == 0, reinterpret_cast<int*>(lds), tok);
   if (c.e < 0) return;
   if (c.n <= 16) {
@@ -373,16 +388,9 @@ __global__ __launch_bounds__(256) void k_moe_quant(MoeArgs a, int P, int IB) {
   const int groups = P * IB;
   const int g = blockIdx.x * 32 + (threadIdx.x >> 3), l8 = threadIdx.x & 7;
   const float4* at = reinterpret_cast<const float4*>(a.h32 + (int64_t)(g < groups ? g : groups - 1) * 128) + l8 * 4;
-  float v[16], s;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 x = at[i];
-    v[4 * i] = x.x;
-    v[4 * i + 1] = x.y;
-    v[4 * i + 2] = x.z;
-    v[4 * i + 3] = x.w;
-  }
-  const uint4 o = quant16(v, &s);
+  const float4 raw[4] = {at[0], at[1], at[2], at[3]};
+  float s;
+  const uint4 o = quant16(raw, &s);
   if (g < groups) {
     reinterpret_cast<uint4*>(a.hq + (int64_t)g * 128)[l8] = o;
     if (l8 == 0) a.hs[(int64_t)(g % IB) * P + g / IB] = s;
@@ -415,7 +423,7 @@ template <int MF, int FN, int PF, int OUT, bool LDSH>
 __global__ __launch_bounds__(kDownThreads, 2) void k_moe_down(MoeArgs a, int cw, int smax, int most) {
   // smax [P][16 FN] results; units (expert, first row, rows); pos and weight
   // per pair; LDSH: scales [P][I / 128] and codes [P][I + 16]
-  extern __shared__ float lds[];
+  extern __shared__ __align__(16) float lds[];
   __shared__ int units_s;   // (not LDSH)
   const int lane = threadIdx.x & 63, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -590,15 +598,8 @@ __global__ __launch_bounds__(kDownThreads, 2) void k_moe_down(MoeArgs a, int cw,
     for (int k = 0; k < kPasses; ++k) {
       const int g = g0 + k * (kDownThreads / 8);
       if (k * (kDownThreads / 8) >= P * IB) break;
-      float v[16], s;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[4 * i] = raw[k][i].x;
-        v[4 * i + 1] = raw[k][i].y;
-        v[4 * i + 2] = raw[k][i].z;
-        v[4 * i + 3] = raw[k][i].w;
-      }
-      const uint4 o = quant16(v, &s);
+      float s;
+      const uint4 o = quant16(raw[k], &s);
       if (g < P * IB) {
         const int row = g / IB;
         reinterpret_cast<uint4*>(lq + row * (I + 16) + (g - row * IB) * 128)[l8] = o;
