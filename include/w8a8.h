@@ -444,8 +444,8 @@ int moe_route_topk(const void* logits, int logits_dtype, const float* bias,
 
 /*
  * A whole mixture-of-experts layer for a few tokens (up to 64; for more,
- * gemm_w8a8_block_grouped over expert-sorted rows), block-wise scheme, in two
- * kernels that read the weights of the chosen experts once:
+ * gemm_w8a8_block_grouped over expert-sorted rows), block-wise scheme, with
+ * the weights of the chosen experts read once:
  *   gate, up = the two halves of A[t] . W_gate_up[e]^T, as gemm_w8a8_block (fp32)
  *   hq, hs   = the group quantiser of gate / (1 + exp(-gate)) * up, taken
  *              from fp32 (no 16-bit rounding between)

@@ -445,3 +445,56 @@ def test_layer_graph_replays_and_streams():
         for k in range(6):
             w = want[(k + i) % 4]
             assert all(_same((outs[i][k][n],), (w[n],)) for n in w)
+
+
+# ----------------------------------------------------------- drawn shapes
+@pytest.mark.parametrize("seed", range(24))
+def test_moe_drawn(seed):
+    """Tokens, slots, experts and sides drawn over the small end of their
+    ranges; skewed ids (some experts take most rows), a share of them empty."""
+    rng = np.random.default_rng(1000 + seed)
+    T, topk, E = int(rng.integers(1, 65)), int(rng.integers(1, 17)), int(2 ** rng.uniform(0, 8))
+    I, K = 128 * int(rng.integers(1, 6)), 128 * int(rng.integers(1, 6))
+    if E * I * K > 1 << 24:
+        E = max(1, (1 << 24) // (I * K))
+    p = rng.random(E) ** 3 + 1e-3
+    ids = rng.choice(E, size=(T, topk), p=p / p.sum())
+    ids[rng.random((T, topk)) < rng.choice([0.0, 0.2, 0.9])] = -1
+    print(f"moe T={T} topk={topk} E={E} I={I} K={K}", flush=True)
+    args = _moe_inputs(T, topk, E, I, K, seed=seed, ids=ids)
+    args[3][ids < 0] = np.nan
+    t = _to(args)
+    got = w8.moe_w8a8_block(*t, out_dtype=torch.float32)
+    _check_moe(args, got, w8.moe_w8a8_block(*t))
+    empty = (ids < 0).all(1)
+    assert not got[torch.from_numpy(empty).to(DEV)].any()
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_norm_drawn(seed):
+    rng = np.random.default_rng(2000 + seed)
+    M, K = int(2 ** rng.uniform(0, 9.5)), 128 * int(2 ** rng.uniform(0, 7.2))
+    dt = [torch.bfloat16, torch.float16][int(rng.integers(2))]
+    d = _norm_inputs(M, K, dt, seed=seed, residual=bool(rng.integers(2)), post=bool(rng.integers(2)),
+                     gate=["none", "channel", "token"][int(rng.integers(3))])
+    scale, scheme = float(rng.uniform(-1, 2)), [w8.W8_SCHEME_BLOCK, w8.W8_SCHEME_CHANNEL][int(rng.integers(2))]
+    print(f"norm M={M} K={K} {dt} {sorted(d)} scale={scale} scheme={scheme}", flush=True)
+    got = w8.norm_residual_quant(**{k: v.to(DEV) for k, v in d.items()}, residual_scale=scale, scheme=scheme,
+                                 normed=True)
+    _check_norm(d, scale, 1e-6, scheme, got, dt)
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_route_drawn(seed):
+    rng = np.random.default_rng(3000 + seed)
+    groups = int(rng.choice([1, 1, 2, 5, 16]))
+    E, T = groups * int(2 ** rng.uniform(0, 10 - np.log2(groups))), int(2 ** rng.uniform(0, 6))
+    kept = int(rng.integers(1, groups + 1))
+    topk = int(rng.integers(1, min(64, kept * (E // groups)) + 1))
+    l = torch.from_numpy(rng.standard_normal((T, E)) * 2).to([torch.float32, torch.bfloat16][int(rng.integers(2))])
+    l[torch.from_numpy(rng.random((T, E)) < rng.choice([0.0, 0.3, 0.95]))] = -float("inf")
+    bias = torch.from_numpy(rng.standard_normal(E) * 0.3).float() if rng.integers(2) else None
+    kw = dict(sigmoid=bool(rng.integers(2)), bias=bias, n_group=groups, topk_group=kept,
+              group_top=int(rng.integers(1, 3)), renormalise=bool(rng.integers(2)), scale=float(rng.uniform(0.5, 3)))
+    print(f"route T={T} E={E} topk={topk} {kw['n_group']}/{kept}", flush=True)
+    _check_route(l, _route(l, topk, **kw), topk, **kw)

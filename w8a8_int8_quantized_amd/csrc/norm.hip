@@ -218,9 +218,9 @@ hipError_t norm_launch(const NormArgs& a, int64_t M, hipStream_t st) {
   if (nch <= 512) return few ? norm_go<FP16, 512, 1>(a, M, st) : norm_go<FP16, 256, 2>(a, M, st);
   if (nch <= 1024) return few ? norm_go<FP16, 1024, 1>(a, M, st) : norm_go<FP16, 512, 2>(a, M, st);
   if (few) return nch <= 2048 ? norm_go<FP16, 1024, 2>(a, M, st) : norm_go<FP16, 1024, 4>(a, M, st);
-  if (nch <= 1536) return norm_go<FP16, 512, 3>(a, M, st);
+  if (nch <= 3 * 512) return norm_go<FP16, 512, 3>(a, M, st);
   if (nch <= 2048) return norm_go<FP16, 512, 4>(a, M, st);
-  return nch <= 3072 ? norm_go<FP16, 1024, 3, true>(a, M, st) : norm_go<FP16, 1024, 4, true>(a, M, st);
+  return nch <= 3 * 1024 ? norm_go<FP16, 1024, 3, true>(a, M, st) : norm_go<FP16, 1024, 4, true>(a, M, st);
 }
 
 }  // namespace
