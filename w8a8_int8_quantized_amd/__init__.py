@@ -130,8 +130,11 @@ def _check(rc, what):
         raise W8Error(f"{what}: {lib.w8_status_string(rc).decode()} (status {rc})", rc)
 
 
-# the current stream's handle without a Stream object around it (3 us less per call)
+# the current stream's handle without a Stream object around it (3 us less per
+# call), and the current device without torch's lazy initialisation (a CUDA
+# tensor is in hand)
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _stream():
@@ -442,11 +445,12 @@ def _dims(t, name, n):
 
 def _run_on(dev, what, fn, *args):
     """The call on dev's current stream, with dev the current device."""
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, _raw_stream(dev.index))
+    i = dev.index
+    if i == _current_device():
+        rc = fn(*args, _raw_stream(i))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, _raw_stream(dev.index))
+            rc = fn(*args, _raw_stream(i))
     if rc:
         _check(rc, what)
 
@@ -486,10 +490,11 @@ def norm_residual_quant(y, pre_weight, residual=None, post_weight=None, gate=Non
         gate_rows = 1 if gate.dim() == 1 else M
         _like(gate, "gate", (K,) if gate.dim() == 1 else (M, K), dt, dev)
     sshape = (M, K // GROUP) if scheme == W8_SCHEME_BLOCK else (M,)
+    # (sizes as arguments of their own cost torch.empty 0.4 us less than a tuple)
     if out is None:
         out = (torch.empty_like(y),)
         if scheme is not None:
-            out += (torch.empty_like(y, dtype=torch.int8), torch.empty(sshape, dtype=torch.float32, device=dev))
+            out += (torch.empty_like(y, dtype=torch.int8), torch.empty(*sshape, dtype=torch.float32, device=dev))
         if normed:
             out += (torch.empty_like(y),)
     else:
@@ -529,11 +534,11 @@ def moe_route_topk(logits, topk, bias=None, score=W8_ROUTE_SOFTMAX, n_group=1, t
     if bias is not None:
         _like(bias, "bias", (E,), torch.float32, dev)
     topk = int(topk)
+    if not 1 <= topk <= E:
+        raise W8Error(f"moe_route_topk: topk must be 1 .. {E}, got {topk}")
     if out is None:
-        if topk < 1:
-            raise W8Error("moe_route_topk: topk must be at least 1")
-        out = (torch.empty((T, topk), dtype=torch.int32, device=dev),
-               torch.empty((T, topk), dtype=torch.float32, device=dev))
+        out = (torch.empty(T, topk, dtype=torch.int32, device=dev),
+               torch.empty(T, topk, dtype=torch.float32, device=dev))
     else:
         _like(out[0], "out ids", (T, topk), torch.int32, dev)
         _like(out[1], "out weights", (T, topk), torch.float32, dev)
@@ -578,13 +583,13 @@ def moe_w8a8_block(A, a_scale, topk_ids, topk_weights, W_gate_up, gate_up_scale,
     _like(W_down, "W_down", (E, K, I), torch.int8, dev)
     _like(down_scale, "down_scale", (E, K // GROUP, I // GROUP), torch.float32, dev)
     if out is None:
-        out = torch.empty((T, K), dtype=out_dtype, device=dev)
+        out = torch.empty(T, K, dtype=out_dtype, device=dev)
     else:
         _like(out, "out", (T, K), out.dtype, dev)
     if out.dtype not in (torch.bfloat16, torch.float32):
         raise W8Error(f"moe_w8a8_block writes bf16 or fp32, not {out.dtype}")
     if workspace is None:
-        workspace = torch.empty((moe_workspace_bytes(T, topk, I, K),), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(moe_workspace_bytes(T, topk, I, K), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise W8Error(f"workspace must be contiguous, on {dev}")
     _run_on(dev, "moe_w8a8_block", lib.moe_w8a8_block, A.data_ptr(), a_scale.data_ptr(), topk_ids.data_ptr(),
