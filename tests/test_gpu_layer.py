@@ -127,18 +127,20 @@ def test_norm_extreme_rows(dt):
     assert not got[1][0].any() and not got[1][2].any()
 
 
-def test_norm_in_place_and_out():
+@pytest.mark.parametrize("M,K", [(37, 1152), (260, 18432)])
+def test_norm_in_place_and_out(M, K):
     """h into the residual's and into y's own memory; rows behind the last one stay."""
-    d = {k: v.to(DEV) for k, v in _norm_inputs(37, 1152, torch.bfloat16, seed=7).items()}
+    d = {k: v.to(DEV) for k, v in _norm_inputs(M, K, torch.bfloat16, seed=7).items()}
     want = w8.norm_residual_quant(**d, normed=True)
     for name in ("residual", "y"):
         g = dict(d)
         g[name] = d[name].clone()
-        bufs = [torch.full((38, 1152), 9, dtype=torch.int8, device=DEV),
-                torch.full((38, 9), 9.0, device=DEV), torch.full((38, 1152), 9.0, dtype=torch.bfloat16, device=DEV)]
-        got = w8.norm_residual_quant(**g, normed=True, out=(g[name], *(b[:37] for b in bufs)))
+        bufs = [torch.full((M + 1, K), 9, dtype=torch.int8, device=DEV),
+                torch.full((M + 1, K // 128), 9.0, device=DEV),
+                torch.full((M + 1, K), 9.0, dtype=torch.bfloat16, device=DEV)]
+        got = w8.norm_residual_quant(**g, normed=True, out=(g[name], *(b[:M] for b in bufs)))
         assert got[0].data_ptr() == g[name].data_ptr() and _same(got, want)
-        assert all(bool((b[37] == 9).all()) for b in bufs)
+        assert all(bool((b[M] == 9).all()) for b in bufs)
 
 
 def test_norm_more_rows_than_a_launch_takes():
@@ -336,6 +338,23 @@ def test_moe_one_expert_takes_all(T, topk):
     args = _moe_inputs(T, topk, 3, 128, 256, seed=9, ids=np.full((T, topk), 1))
     t = _to(args)
     _check_moe(args, w8.moe_w8a8_block(*t, out_dtype=torch.float32), w8.moe_w8a8_block(*t))
+
+
+def test_moe_weights_beyond_four_gigabytes():
+    """160 experts of K = 7168, I = 2048 (4.7 GB of W_gate_up): the last ones
+    against the oracle on their own weights."""
+    T, topk, E, I, K = 2, 2, 160, 2048, 7168
+    used = [3, 158, 159]
+    small = _moe_inputs(T, topk, len(used), I, K, seed=8, ids=[[2, 0], [1, 2]])
+    A, sa, ids, wt, w13, s13, w2, s2 = _to(small)
+    big = []
+    for v in (w13, s13, w2, s2):
+        full = torch.ones(E, *v.shape[1:], dtype=v.dtype, device=DEV)
+        full[used] = v
+        big.append(full)
+    at = torch.tensor(used, dtype=torch.int32, device=DEV)[ids.long()]
+    got = w8.moe_w8a8_block(A, sa, at, wt, *big, out_dtype=torch.float32)
+    _check_moe(small, got, w8.moe_w8a8_block(A, sa, at, wt, *big))
 
 
 def test_moe_none_chosen():
