@@ -433,7 +433,8 @@ int norm_residual_quant(const void* y, const void* residual, const void* post_we
  * group's score and is never chosen.  Slots that find no expert (fewer than
  * topk are left, down to none) hold id -1 and weight 0.  +inf counts as the
  * largest finite fp32.
- * E <= 1024, topk <= 64 and <= topk_group * E / n_group, E % n_group == 0.
+ * E <= 1024, topk <= 64 and <= topk_group * E / n_group, n_group <= 64,
+ * E % n_group == 0.
  */
 enum w8_route_score { W8_ROUTE_SOFTMAX = 0, W8_ROUTE_SIGMOID = 1 };
 

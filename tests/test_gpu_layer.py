@@ -187,7 +187,7 @@ def _route(logits, topk, sigmoid=False, bias=None, **kw):
 @pytest.mark.parametrize("T,E,topk,n_group,topk_group", [
     (1, 1, 1, 1, 1), (3, 2, 2, 1, 1), (5, 8, 2, 1, 1), (9, 61, 6, 1, 1), (4, 64, 8, 8, 4), (7, 65, 5, 1, 1),
     (17, 128, 8, 4, 2), (3, 160, 6, 8, 3), (33, 256, 8, 8, 4), (2, 300, 60, 1, 1), (2, 512, 10, 16, 3),
-    (3, 1024, 64, 1, 1), (2, 1023, 7, 1, 1), (2, 1024, 3, 1024, 5), (6, 12, 12, 4, 4)])
+    (3, 1024, 64, 1, 1), (2, 1023, 7, 1, 1), (2, 1024, 3, 64, 5), (3, 63, 2, 63, 9), (4, 96, 5, 32, 7), (3, 40, 4, 20, 3), (6, 12, 12, 4, 4)])
 def test_route(T, E, topk, n_group, topk_group, dt):
     g = _gen(T + E)
     logits = (2 * torch.randn(T, E, generator=g)).to(dt)

@@ -56,6 +56,7 @@ def test_route_argument_checks():
     assert _route(topk=0) == ESHAPE and _route(topk=65, E=1024, topk_group=4) == ESHAPE
     assert _route(topk=9) == ESHAPE                    # two groups of four stay
     assert _route(n_group=3) == ESHAPE and _route(n_group=0) == ESHAPE
+    assert _route(E=1024, n_group=128) == ESHAPE
     assert _route(topk_group=5) == ESHAPE and _route(topk_group=0) == ESHAPE
     assert _route(group_top=3) == EVAL and _route(scale=float("nan")) == EVAL
     assert _route(logits=N) == ENULL and _route(ids=N) == ENULL and _route(w=N) == ENULL

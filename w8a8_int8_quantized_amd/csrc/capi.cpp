@@ -399,7 +399,7 @@ int moe_route_topk(const void* logits, int logits_dtype, const float* bias, int 
   if (score != W8_ROUTE_SOFTMAX && score != W8_ROUTE_SIGMOID) return W8_ERR_DTYPE;
   if (T < 0 || T > kMaxRows || E < 1 || E > w8::kRouteMaxE || topk < 1 || topk > w8::kRouteMaxTopk)
     return W8_ERR_SHAPE;
-  if (n_group < 1 || E % n_group != 0 || topk_group < 1 || topk_group > n_group) return W8_ERR_SHAPE;
+  if (n_group < 1 || n_group > w8::kRouteMaxGroups || E % n_group != 0 || topk_group < 1 || topk_group > n_group) return W8_ERR_SHAPE;
   if (topk > topk_group * (E / n_group)) return W8_ERR_SHAPE;
   if (group_top != 1 && group_top != 2) return W8_ERR_VALUE;
   if (!(scale >= -3.4e38 && scale <= 3.4e38)) return W8_ERR_VALUE;

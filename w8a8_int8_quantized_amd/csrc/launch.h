@@ -91,10 +91,11 @@ struct RouteArgs {
   int E, topk, n_group, topk_group, group_top, dtype;   // dtype: a w8_dtype
   bool sigmoid, renormalise;
   int64_t t0;           // set by the launcher: the launch's first token
-  uint32_t per_magic;   // set by the launcher: e / (E / n_group) = e * per_magic >> 20
+  int per, lg_w;        // and the experts of a group, the lanes to a group (log2),
+  uint32_t per_magic;   // and e / per = e * per_magic >> 20
 };
 hipError_t launch_route_topk(RouteArgs a, int64_t T, hipStream_t st);
-constexpr int64_t kRouteMaxE = 1024, kRouteMaxTopk = 64;
+constexpr int64_t kRouteMaxE = 1024, kRouteMaxTopk = 64, kRouteMaxGroups = 64;
 
 // A mixture-of-experts layer for a few tokens (moe.hip).  h32 .. start (out32 among them) lie in
 // the caller's workspace: moe_workspace gives its size and, with a and ws,

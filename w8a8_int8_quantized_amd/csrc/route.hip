@@ -17,7 +17,7 @@
 // split into two words: the largest high word is found with four DPP steps
 // and four scalar maxima, and only experts that tie in it are compared in the
 // low word.  Bound by latency and by the 64-bit exp: one token of 256 experts
-// 5.9 us, 4096 tokens 10.9 us (a workgroup per token that counted the better
+// 5.4 us, 4096 tokens 10.8 us (a workgroup per token that counted the better
 // experts for each took 10.8 and 52 us).
 #include "common.h"
 #include "launch.h"
@@ -43,8 +43,16 @@ __device__ __forceinline__ double lane_double(double v, int lane) {
   return __builtin_bit_cast(double, lo | (hi << 32));
 }
 
+template <int CTRL>
+__device__ __forceinline__ double dpp_double(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xF, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
+}
+
 // NE: elements per lane (E <= 64 NE).  Dynamic LDS: c [E] and s [E], then
-// (n_group > 1) the groups' scores [n_group] and a byte each.
+// (n_group > 1) the groups' scores [n_group].
 template <int NE>
 __global__ __launch_bounds__(64) void k_route_topk(RouteArgs a) {
   extern __shared__ __align__(16) double lds[];
@@ -53,7 +61,6 @@ __global__ __launch_bounds__(64) void k_route_topk(RouteArgs a) {
   double* lc = lds;
   double* lw = lc + E;
   double* gs = lw + E;
-  uint8_t* stays = reinterpret_cast<uint8_t*>(gs + a.n_group);
   const double ninf = -__builtin_inf();
 
   float lf[NE], bias[NE];
@@ -112,44 +119,40 @@ __global__ __launch_bounds__(64) void k_route_topk(RouteArgs a) {
   }
   __syncthreads();   // one wave: orders its LDS accesses only
   if (a.n_group > 1) {
-    const int per = E / a.n_group;
     // w lanes to a group take every w-th of its experts, then join
-    int w = 1;
-    while (w * 2 * a.n_group <= 64) w *= 2;
-    for (int g0 = 0; g0 < a.n_group; g0 += 64 / w) {
-      const int g = g0 + lane / w;
-      double b1 = ninf, b2 = ninf;
-      if (g < a.n_group)
-        for (int j = lane & (w - 1); j < per; j += w) {
-          const double v = lc[g * per + j];
-          if (v > b1) {
-            b2 = b1;
-            b1 = v;
-          } else if (v > b2) {
-            b2 = v;
-          }
-        }
-      for (int d = 1; d < w; d <<= 1) {
-        const double o1 = __shfl_xor(b1, d, 64), o2 = __shfl_xor(b2, d, 64);
-        const double low = o1 < b1 ? o1 : b1, second = o2 > b2 ? o2 : b2;
-        b1 = o1 > b1 ? o1 : b1;
-        b2 = low > second ? low : second;
+    const int per = a.per, w = 1 << a.lg_w, g = lane >> a.lg_w;
+    double b1 = ninf, b2 = ninf;
+    if (g < a.n_group)
+      for (int j = lane & (w - 1); j < per; j += w) {
+        const double v = lc[g * per + j];
+        b2 = fmax(b2, fmin(b1, v));
+        b1 = fmax(b1, v);
       }
-      if (g < a.n_group && (lane & (w - 1)) == 0) gs[g] = a.group_top == 2 && b2 > ninf ? b1 + b2 : b1;
-    }
+    auto join = [&](double o1, double o2) {
+      b2 = fmax(fmin(b1, o1), fmax(b2, o2));
+      b1 = fmax(b1, o1);
+    };
+    // each step's partner holds the same as its neighbours that joined before
+    if (w > 1) join(dpp_double<0xB1>(b1), dpp_double<0xB1>(b2));     // quad_perm [1,0,3,2]
+    if (w > 2) join(dpp_double<0x4E>(b1), dpp_double<0x4E>(b2));     // quad_perm [2,3,0,1]
+    if (w > 4) join(dpp_double<0x141>(b1), dpp_double<0x141>(b2));   // row_half_mirror
+    if (w > 8) join(dpp_double<0x128>(b1), dpp_double<0x128>(b2));   // row_ror:8
+    if (w > 16) join(__shfl_xor(b1, 16, 64), __shfl_xor(b2, 16, 64));
+    if ((lane & (w - 1)) == 0 && g < a.n_group) gs[g] = a.group_top == 2 && b2 > ninf ? b1 + b2 : b1;
     __syncthreads();
-    for (int g = lane; g < a.n_group; g += 64) {
-      const double v = gs[g];
-      int place = 0;
-      for (int j = 0; j < a.n_group; ++j) place += gs[j] > v || (gs[j] == v && j < g);
-      stays[g] = place < a.topk_group;
+    // lane g: the place of group g; a bit per group that stays
+    const double v = lane < a.n_group ? gs[lane] : ninf;
+    int place = 0;
+    for (int j = 0; j < a.n_group; ++j) {
+      const double o = lane_double(v, j);
+      place += (int)(o > v) | ((int)(o == v) & (int)(j < lane));
     }
-    __syncthreads();
+    const uint64_t stays = __ballot(lane < a.n_group && place < a.topk_group);
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
       const int e = i * 64 + lane;
       // e / per: exact for e < 1024 and per < 1024
-      if (e < E && !stays[((uint32_t)e * a.per_magic) >> 20]) c[i] = ninf;
+      if (!(stays >> (((uint32_t)e * a.per_magic) >> 20) & 1)) c[i] = ninf;
     }
   }
 
@@ -208,7 +211,7 @@ __global__ __launch_bounds__(64) void k_route_topk(RouteArgs a) {
 
 template <int NE>
 hipError_t route_launch(RouteArgs a, int64_t T, hipStream_t st) {
-  const size_t lds = (size_t)a.E * 16 + (a.n_group > 1 ? (size_t)a.n_group * 9 : 0);
+  const size_t lds = (size_t)a.E * 16 + (a.n_group > 1 ? (size_t)a.n_group * 8 : 0);
   constexpr int64_t kPart = int64_t(1) << 24;   // a launch holds fewer than 2^32 threads
   for (a.t0 = 0; a.t0 < T; a.t0 += kPart) {
     const int64_t n = T - a.t0 < kPart ? T - a.t0 : kPart;
@@ -222,7 +225,9 @@ hipError_t route_launch(RouteArgs a, int64_t T, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_route_topk(RouteArgs a, int64_t T, hipStream_t st) {
-  const int per = a.E / a.n_group;
+  const int per = a.per = a.E / a.n_group;
+  a.lg_w = 0;
+  while ((2 << a.lg_w) * a.n_group <= 64) ++a.lg_w;
   a.per_magic = (uint32_t)(((1 << 20) + per - 1) / per);
   if (a.E <= 64) return route_launch<1>(a, T, st);
   if (a.E <= 128) return route_launch<2>(a, T, st);
