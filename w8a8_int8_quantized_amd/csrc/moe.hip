@@ -415,6 +415,21 @@ constexpr int64_t kLdsPairs = 64, kLdsCodes = 32768;
 // Up to this K the experts may be split over workgroups.
 constexpr int64_t kSplitMaxK = 4096;
 
+// The S places of n float4s each into the first, in their order.
+template <int S>
+__device__ __forceinline__ void join_places(float* lds, int n) {
+  v4f* at = reinterpret_cast<v4f*>(lds);
+  for (int i = threadIdx.x; i < n; i += kDownThreads) {
+    v4f o[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) o[s] = at[s * n + i];
+#pragma unroll
+    for (int s = 1; s < S; ++s) o[0] += o[s];
+    at[i] = o[0];
+  }
+  __syncthreads();
+}
+
 // LDSH (few pairs): every workgroup quantises the h of all pairs into LDS
 // (rows of I + 16 bytes, so that the 16 rows of a fragment read lie in
 // different banks) while its first weights are on their way; else k_moe_quant
@@ -668,14 +683,19 @@ __global__ __launch_bounds__(kDownThreads, 2) void k_moe_down(MoeArgs a, int cw,
     }
   }
   __syncthreads();
+  // the places of each pair's row into the first
+  switch (smax) {
+    case 2: join_places<2>(lds, P * 4 * FN); break;
+    case 4: join_places<4>(lds, P * 4 * FN); break;
+    case 8: join_places<8>(lds, P * 4 * FN); break;
+    default: break;
+  }
   if (gridDim.y > 1) {   // k_moe_combine sums the pairs
     for (int k = wave; k < u_n; k += kDownWaves) {
       const Unit c = unit(u_lo + k);
       for (int i = lane; i < c.rows * cols; i += 64) {
         const int r = i / cols, col = i - r * cols;
-        float o = lds[(c.base + r) * 16 * FN + col];
-        for (int s = 1; s < smax; ++s) o += lds[(s * P + c.base + r) * 16 * FN + col];
-        a.out32[(int64_t)(c.base + r) * a.K + n0 + col] = o;
+        a.out32[(int64_t)(c.base + r) * a.K + n0 + col] = lds[(c.base + r) * 16 * FN + col];
       }
     }
     return;
@@ -683,12 +703,19 @@ __global__ __launch_bounds__(kDownThreads, 2) void k_moe_down(MoeArgs a, int cw,
   for (int i = threadIdx.x; i < a.T * cols; i += kDownThreads) {
     const int t = i / cols, col = i - t * cols;
     float y = 0.f;
-    for (int j = 0; j < a.topk; ++j) {
-      const int p = t * a.topk + j, r = pos[p];
-      if (r < 0) continue;
-      float o = lds[r * 16 * FN + col];
-      for (int s = 1; s < smax; ++s) o += lds[(s * P + r) * 16 * FN + col];
-      y = __builtin_fmaf(wt[p], o, y);
+    for (int j0 = 0; j0 < a.topk; j0 += 4) {   // four slots' LDS reads at a time
+      int r[4];
+      float w[4], o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int p = t * a.topk + (j0 + j < a.topk ? j0 + j : a.topk - 1);
+        r[j] = j0 + j < a.topk ? pos[p] : -1;
+        w[j] = wt[p];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = lds[(r[j] < 0 ? 0 : r[j]) * 16 * FN + col];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y = r[j] < 0 ? y : __builtin_fmaf(w[j], o[j], y);
     }
     const int64_t at = (int64_t)t * a.K + n0 + col;
     if (OUT == OUT_F32)
