@@ -16,8 +16,8 @@
 // kernel itself where the pairs are few, else by k_moe_quant; where the output
 // has few columns, k_moe_combine sums what several down workgroups share.
 // 64 tokens, K = 7168, I = 2048, 64 experts, 8 of them per token (2.8 GB of
-// weights, each byte fetched once by the counters): 314 + 5 + 163 us, 6.0 and
-// 5.8 TB/s; one token (352 MB): 43 + 27 us.  A "pair" is one slot of one token (t, j), p = t topk + j; the pairs of one
+// weights, each byte fetched once by the counters): 313 + 5 + 162 us, 6.0 and
+// 5.8 TB/s; one token (352 MB): 43 + 26 us.  A "pair" is one slot of one token (t, j), p = t topk + j; the pairs of one
 // expert are the rows of its products, in the order of p, and the rows of all
 // experts in the order of the expert index are the rows of hq.  A pair whose
 // id is outside 0 .. E - 1 has no row.

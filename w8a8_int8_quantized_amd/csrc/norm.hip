@@ -90,7 +90,7 @@ struct Row {
 // t + NT, ... (CH of them at most), so the row is read once and stays in
 // registers through both norms and the quantiser.  A 128-value group is the
 // 16 chunks of 16 neighbouring lanes.  HBM-bound: 4096 x 7168 with residual,
-// both norms and group codes 41 us, 206 MB at 5.0 TB/s; one row 4.5 us.
+// both norms and group codes 42 us, 206 MB at 4.9 TB/s; one row 4.5 us.
 // (The same in 64-bit arithmetic throughout takes 58 and 6.4 us.)
 // LATE: all but y is loaded where it is used instead, which leaves registers
 // for two workgroups of 1024 threads per CU.

@@ -17,7 +17,7 @@
 // split into two words: the largest high word is found with four DPP steps
 // and four scalar maxima, and only experts that tie in it are compared in the
 // low word.  Bound by latency and by the 64-bit exp: one token of 256 experts
-// 5.4 us, 4096 tokens 10.8 us (a workgroup per token that counted the better
+// 5.5 us, 4096 tokens 10.6 us (a workgroup per token that counted the better
 // experts for each took 10.8 and 52 us).
 #include "common.h"
 #include "launch.h"
