@@ -97,9 +97,9 @@ struct RouteArgs {
 hipError_t launch_route_topk(RouteArgs a, int64_t T, hipStream_t st);
 constexpr int64_t kRouteMaxE = 1024, kRouteMaxTopk = 64, kRouteMaxGroups = 64;
 
-// A mixture-of-experts layer for a few tokens (moe.hip).  h32 .. start (out32 among them) lie in
-// the caller's workspace: moe_workspace gives its size and, with a and ws,
-// sets them.
+// A mixture-of-experts layer for a few tokens (moe.hip).  The pointers from
+// h32 to start lie in the caller's workspace: moe_workspace gives its size
+// and, with a and ws, sets them.
 struct MoeArgs {
   const int8_t* A;
   const float* sa;
