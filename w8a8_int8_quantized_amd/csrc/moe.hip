@@ -848,10 +848,10 @@ int64_t moe_workspace(int64_t T, int64_t topk, int64_t I, int64_t K, MoeArgs* a,
 hipError_t launch_moe_block(const MoeArgs& a, OutKind out, hipStream_t st) {
   const int P = a.T * a.topk, IB = a.I / 128;
   const int most = P < a.E ? P : a.E;   // chosen experts, at most
-  // gate_up: experts of many rows four fragments of rows at a time (8 experts of
-  // 64 rows: 73 us, two at a time reads the weights twice), others two, which
-  // leaves registers for four workgroups per CU (16 to 23 rows: 52 us, 66 with
-  // four).  Columns per workgroup: 32 load the activations half as often as
+  // gate_up: experts of many rows four fragments of rows at a time, two
+  // workgroups per CU (8 experts of 64 rows: 73 us, 94 with 16 columns and
+  // three); others two fragments and four workgroups (16 to 23 rows: 52 us, 66
+  // with four fragments and 16 columns).  Columns per workgroup: 32 load the activations half as often as
   // 16, which spread few columns more evenly (one token of 8 experts,
   // K = 7168, I = 2048: 43 us with 32, 45 with 16; 7 experts, I = 256: 21 and
   // 16); 64, with half the waves per column, for short K, where a workgroup's
