@@ -52,19 +52,22 @@ __device__ __forceinline__ float block_max(float v, float* red) {
   return r;
 }
 
-// 8 fp32 values to the 16-bit type (round to nearest even), packed.
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+
+// 8 fp32 values to the 16-bit type (round to nearest even), packed: one
+// conversion instruction for two values.
 template <bool FP16>
 __device__ __forceinline__ uint4 pack8(const float* v) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (FP16) {
-      const uint16_t a = __builtin_bit_cast(uint16_t, (_Float16)v[2 * i]);
-      const uint16_t b = __builtin_bit_cast(uint16_t, (_Float16)v[2 * i + 1]);
-      w[i] = (uint32_t)a | ((uint32_t)b << 16);
-    } else {
-      w[i] = f32_to_bf16_rne(v[2 * i]) | (f32_to_bf16_rne(v[2 * i + 1]) << 16);
-    }
+    const v2f x = {v[2 * i], v[2 * i + 1]};
+    if (FP16)
+      w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, v2h));
+    else
+      w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, v2b));
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -90,8 +93,9 @@ struct Row {
 // t + NT, ... (CH of them at most), so the row is read once and stays in
 // registers through both norms and the quantiser.  A 128-value group is the
 // 16 chunks of 16 neighbouring lanes.  HBM-bound: 4096 x 7168 with residual,
-// both norms and group codes 42 us, 206 MB at 4.9 TB/s; one row 4.5 us.
-// (The same in 64-bit arithmetic throughout takes 58 and 6.4 us.)
+// both norms and group codes 41 us, 206 MB at 5.0 TB/s; one row 4.5 us.
+// (The same in 64-bit arithmetic throughout takes 58 and 6.4 us, and as much
+// where only values near a border of the 16-bit type are done again in 64.)
 // LATE: all but y is loaded where it is used instead, which leaves registers
 // for two workgroups of 1024 threads per CU.
 template <bool FP16, int NT, int CH, bool LATE>
@@ -103,6 +107,13 @@ __global__ __launch_bounds__(NT, LATE ? 8 : 1) void k_norm_residual_quant(NormAr
   const Row y(a.y, row, a.K), res(a.residual, row, a.K), gate(a.gate, a.gate_rows == 1 ? 0 : row, a.K),
       pw(a.post_weight, 0, a.K), nw(a.pre_weight, 0, a.K);
   const float inv_k = 1.0f / (float)a.K;
+
+  // whether this wave has any of the row's i-th chunks: in the wide shapes,
+  // waves past the row's end skip the arithmetic (one row of 18432: 7.5 us
+  // against 8.1; in the narrow ones the branches cost more than they save,
+  // 4096 x 7168 41.6 us against 41.0)
+  const int first = __builtin_amdgcn_readfirstlane((int)threadIdx.x & ~63);
+  auto inside = [&](int i) { return NT * CH <= 1024 || first + NT * i < nch; };
 
   constexpr int CE = LATE ? 1 : CH;
   uint4 raw[CH], rr[CE], rg[CE], rp[CE], rn[CE];
@@ -121,6 +132,7 @@ __global__ __launch_bounds__(NT, LATE ? 8 : 1) void k_norm_residual_quant(NormAr
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
+      if (!inside(i)) break;
       float v[8];
       unpack8<FP16>(raw[i], v);
 #pragma unroll
@@ -131,6 +143,7 @@ __global__ __launch_bounds__(NT, LATE ? 8 : 1) void k_norm_residual_quant(NormAr
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
+    if (!inside(i)) break;
     const int c = threadIdx.x + NT * i;
     float v[8], o[8];
     unpack8<FP16>(raw[i], v);
@@ -159,6 +172,7 @@ __global__ __launch_bounds__(NT, LATE ? 8 : 1) void k_norm_residual_quant(NormAr
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
+    if (!inside(i)) break;
     const int c = threadIdx.x + NT * i;
     float v[8], o[8];
     unpack8<FP16>(raw[i], v);
@@ -176,6 +190,7 @@ __global__ __launch_bounds__(NT, LATE ? 8 : 1) void k_norm_residual_quant(NormAr
   if (!group) amax = block_max<NW>(amax, red[2]);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
+    if (!inside(i)) break;
     const int c = threadIdx.x + NT * i;
     // a group's 16 lanes are all inside the row or all outside it
     const QScale sc = make_scale(group ? max16(am[i]) : amax);
@@ -217,7 +232,8 @@ hipError_t norm_launch(const NormArgs& a, int64_t M, hipStream_t st) {
   if (nch <= 256) return norm_go<FP16, 256, 1>(a, M, st);
   if (nch <= 512) return few ? norm_go<FP16, 512, 1>(a, M, st) : norm_go<FP16, 256, 2>(a, M, st);
   if (nch <= 1024) return few ? norm_go<FP16, 1024, 1>(a, M, st) : norm_go<FP16, 512, 2>(a, M, st);
-  if (few) return nch <= 2048 ? norm_go<FP16, 1024, 2>(a, M, st) : norm_go<FP16, 1024, 4>(a, M, st);
+  if (few && nch <= 2048) return norm_go<FP16, 1024, 2>(a, M, st);
+  if (few) return nch <= 3 * 1024 ? norm_go<FP16, 1024, 3>(a, M, st) : norm_go<FP16, 1024, 4>(a, M, st);
   if (nch <= 3 * 512) return norm_go<FP16, 512, 3>(a, M, st);
   if (nch <= 2048) return norm_go<FP16, 512, 4>(a, M, st);
   return nch <= 3 * 1024 ? norm_go<FP16, 1024, 3, true>(a, M, st) : norm_go<FP16, 1024, 4, true>(a, M, st);
