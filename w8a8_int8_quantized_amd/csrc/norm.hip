@@ -224,7 +224,10 @@ hipError_t norm_go(NormArgs a, int64_t M, hipStream_t st) {
 
 // Few rows leave CUs idle: the row is spread as thin as it goes.  With more
 // rows fewer and fuller threads win (K = 4096: 333 rows 6.2 us with 512
-// threads x 1 chunk against 6.4 with 256 x 2, 4096 rows 23.0 against 20.6).
+// threads x 1 chunk against 6.4 with 256 x 2, 4096 rows 23.0 against 20.6;
+// K = 8320: 1023 rows 28 us with 1024 x 2 against 17 with 512 x 3; K = 18432:
+// one row 10.1 us with 1024 x 4 against 7.4 with 1024 x 3, 1023 rows 42 us with
+// every load first against 28 LATE).
 template <bool FP16>
 hipError_t norm_launch(const NormArgs& a, int64_t M, hipStream_t st) {
   const int nch = a.K >> 3;
