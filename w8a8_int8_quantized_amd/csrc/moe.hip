@@ -336,25 +336,21 @@ __device__ __forceinline__ void gate_up_rows(const MoeArgs& a, const Chosen& c, 
   v4f acc[2 * FC][MF];
   gate_up_sums<MF, FC, PF, WK>(a, c.e, c0, part, r0, c.n, tok, sx, sw, stage, acc);
   __syncthreads();   // the scales' place is free
-  if constexpr (WK > 1) {
-    v4f* red = reinterpret_cast<v4f*>(lds) + tile * (WK - 1) * 2 * FC * MF * 64;
-    if (part > 0) {
+  v4f* red = reinterpret_cast<v4f*>(lds) + tile * (WK - 1) * 2 * FC * MF * 64;
+  if (part > 0) {
+#pragma unroll
+    for (int f = 0; f < 2 * FC; ++f)
+#pragma unroll
+      for (int j = 0; j < MF; ++j) red[(((part - 1) * 2 * FC + f) * MF + j) * 64 + lane] = acc[f][j];
+  }
+  __syncthreads();
+  if (part == 0) {
+#pragma unroll
+    for (int w = 0; w < WK - 1; ++w)
 #pragma unroll
       for (int f = 0; f < 2 * FC; ++f)
 #pragma unroll
-        for (int j = 0; j < MF; ++j) red[(((part - 1) * 2 * FC + f) * MF + j) * 64 + lane] = acc[f][j];
-    }
-    __syncthreads();
-    if (part == 0) {
-#pragma unroll
-      for (int w = 0; w < WK - 1; ++w)
-#pragma unroll
-        for (int f = 0; f < 2 * FC; ++f)
-#pragma unroll
-          for (int j = 0; j < MF; ++j) acc[f][j] += red[((w * 2 * FC + f) * MF + j) * 64 + lane];
-    }
-  }
-  if (part == 0) {
+        for (int j = 0; j < MF; ++j) acc[f][j] += red[((w * 2 * FC + f) * MF + j) * 64 + lane];
 #pragma unroll
     for (int j = 0; j < MF; ++j) {
       const int r = r0 + 16 * j + (lane & 15);
