@@ -92,7 +92,7 @@ struct RouteArgs {
   bool sigmoid, renormalise;
   int64_t t0;           // set by the launcher: the launch's first token
   int per, lg_w;        // and the experts of a group, the lanes to a group (log2),
-  uint32_t per_magic;   // and e / per = e * per_magic >> 20
+  uint32_t per_magic;   // and route_group_magic(per)
 };
 hipError_t launch_route_topk(RouteArgs a, int64_t T, hipStream_t st);
 constexpr int64_t kRouteMaxE = 1024, kRouteMaxTopk = 64, kRouteMaxGroups = 64;

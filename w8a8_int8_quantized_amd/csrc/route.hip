@@ -21,6 +21,7 @@
 // experts for each took 10.8 and 52 us).
 #include "common.h"
 #include "launch.h"
+#include "route_groups.h"
 
 namespace w8 {
 namespace {
@@ -151,8 +152,7 @@ __global__ __launch_bounds__(64) void k_route_topk(RouteArgs a) {
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
       const int e = i * 64 + lane;
-      // e / per: exact for e < 1024 and per < 1024
-      if (!(stays >> (((uint32_t)e * a.per_magic) >> 20) & 1)) c[i] = ninf;
+      if (!route_group_stays(stays, (uint32_t)e, (uint32_t)E, a.per_magic)) c[i] = ninf;
     }
   }
 
@@ -228,7 +228,7 @@ hipError_t launch_route_topk(RouteArgs a, int64_t T, hipStream_t st) {
   const int per = a.per = a.E / a.n_group;
   a.lg_w = 0;
   while ((2 << a.lg_w) * a.n_group <= 64) ++a.lg_w;
-  a.per_magic = (uint32_t)(((1 << 20) + per - 1) / per);
+  a.per_magic = route_group_magic((uint32_t)per);
   if (a.E <= 64) return route_launch<1>(a, T, st);
   if (a.E <= 128) return route_launch<2>(a, T, st);
   if (a.E <= 256) return route_launch<4>(a, T, st);
