@@ -130,11 +130,17 @@ def _check(rc, what):
         raise W8Error(f"{what}: {lib.w8_status_string(rc).decode()} (status {rc})", rc)
 
 
+def _public_raw_stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
 # the current stream's handle without a Stream object around it (3 us less per
 # call), and the current device without torch's lazy initialisation (a CUDA
-# tensor is in hand)
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# tensor is in hand).  Both names are torch's own: a torch without them (one
+# built without GPU support has none, and still makes the argument checks and
+# size queries) takes the public calls
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_raw_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream():
