@@ -5,9 +5,42 @@ import pytest
 import torch
 
 import w8a8_int8_quantized_amd as w8
-from test_gpu_layer import DEV, _check_route, _gen, _norm_inputs, _route, _same
+from test_gpu_layer import DEV, _check_norm, _check_route, _gen, _norm_inputs, _route, _same
 
 pytestmark = pytest.mark.gpu
+
+
+# -------------------------------------------------------------------- norm
+# More than 256 rows, so that each of the launch shapes for many rows is taken:
+# threads x chunks 256 x 1, 256 x 2, 512 x 2, 512 x 3, 512 x 4, and with the
+# later loads 1024 x 3 and 1024 x 4 (a size in each shape's middle or at its
+# border).  A thread's squares are at most 32, as the tolerances count.
+MANY_ROWS = [1024, 2176, 4224, 8320, 12288, 12416, 16384, 16512, 18432, 24704, 32768]
+
+
+@pytest.mark.parametrize("scheme", [w8.W8_SCHEME_BLOCK, w8.W8_SCHEME_CHANNEL])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("K", MANY_ROWS)
+def test_norm_many_rows(K, dt, scheme):
+    print(f"norm M=257 K={K} {dt} scheme={scheme}", flush=True)
+    d = _norm_inputs(257, K, dt, seed=K, gate="token" if scheme == w8.W8_SCHEME_BLOCK else "channel")
+    got = w8.norm_residual_quant(**{k: v.to(DEV) for k, v in d.items()}, residual_scale=0.37, eps=1e-5, scheme=scheme,
+                                 normed=True)
+    _check_norm(d, 0.37, 1e-5, scheme, got, dt)
+
+
+@pytest.mark.parametrize("K", [8320, 18432, 32768])
+@pytest.mark.parametrize("name", ["residual", "y"])
+def test_norm_many_rows_in_place(K, name):
+    """h into the memory of an input that the later loads read: against the oracle."""
+    d = _norm_inputs(257, K, torch.bfloat16, seed=K + 1)
+    g = {k: v.to(DEV) for k, v in d.items()}
+    M = 257
+    out = (g[name], torch.empty(M, K, dtype=torch.int8, device=DEV), torch.empty(M, K // 128, device=DEV),
+           torch.empty(M, K, dtype=torch.bfloat16, device=DEV))
+    got = w8.norm_residual_quant(**g, residual_scale=-0.6, normed=True, out=out)
+    assert got[0].data_ptr() == g[name].data_ptr()
+    _check_norm(d, -0.6, 1e-6, w8.W8_SCHEME_BLOCK, got, torch.bfloat16)
 
 
 # ------------------------------------------------------------------ router
