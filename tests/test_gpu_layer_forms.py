@@ -1,11 +1,14 @@
 """GPU parity of the layer entry points in forms and sizes that
 test_gpu_layer.py does not reach, with its oracle, checks and tolerances."""
 
+import numpy as np
 import pytest
 import torch
 
+import moe_forms
 import w8a8_int8_quantized_amd as w8
-from test_gpu_layer import DEV, _check_norm, _check_route, _gen, _norm_inputs, _route, _same
+from test_gpu_layer import (DEV, _check_moe, _check_norm, _check_route, _gen, _moe_inputs, _norm_inputs, _route,
+                            _same, _to)
 
 pytestmark = pytest.mark.gpu
 
@@ -53,6 +56,23 @@ def test_route_lanes_past_the_last_expert(E, n_group):
             kw = dict(sigmoid=sigmoid, n_group=n_group, topk_group=kept, bias=0.1 * torch.randn(E, generator=_gen(3)))
             topk = min(5, kept * (E // n_group))
             _check_route(logits, _route(logits, topk, **kw), topk, **kw)
+
+
+# ----------------------------------------------------------------- experts
+@pytest.mark.parametrize("case", moe_forms.CASES, ids=lambda c: "x".join(str(v) for v in c[:5]))
+def test_moe_forms(case):
+    """Every form of the kernels, with experts of many rows among experts of few."""
+    print(f"moe {case}", flush=True)
+    T, topk, E, I, K = case[:5]
+    ids = moe_forms.ids_of(case)
+    args = _moe_inputs(T, topk, E, I, K, seed=T + topk + E, ids=ids)
+    args[3][ids < 0] = np.nan
+    t = _to(args)
+    ws = torch.full((w8.moe_workspace_bytes(T, topk, I, K),), 0xFF, dtype=torch.uint8, device=DEV)
+    buf = torch.full((T + 1, K), 5.0, device=DEV)
+    got = w8.moe_w8a8_block(*t, out=buf[:T], workspace=ws)
+    _check_moe(args, got, w8.moe_w8a8_block(*t))
+    assert bool((buf[T] == 5).all())
 
 
 # ------------------------------------------------------------------ binding

@@ -21,17 +21,13 @@
 // expert are the rows of its products, in the order of p, and the rows of all
 // experts in the order of the expert index are the rows of hq.  A pair whose
 // id is outside 0 .. E - 1 has no row.
-#include <type_traits>
-
 #include "common.h"
 #include "launch.h"
+#include "moe_plan.h"
 
 namespace w8 {
 namespace {
 
-constexpr int kMaxPairs = 1024;
-template <int N>
-using Int = std::integral_constant<int, N>;
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
 // Added to the offset of a load that must read zero: beyond the range of
@@ -169,7 +165,7 @@ __device__ __forceinline__ uint4 quant16(const float4* raw, float* scale) {
 }
 
 // ---------------------------------------------------- who has which expert
-constexpr int kGuWaves = 4, kGuThreads = 64 * kGuWaves;
+constexpr int kGuThreads = 64 * kGuWaves;
 constexpr int kPerThread = kMaxPairs / kGuThreads;
 
 struct Chosen {
@@ -403,16 +399,7 @@ __global__ __launch_bounds__(256) void k_moe_quant(MoeArgs a, int P, int IB) {
 // granule there, in LDS, so no two waves write the same one.  Then every
 // output sums its token's slots in slot order: no atomics, the same bits
 // every time.
-constexpr int kDownWaves = 8, kDownThreads = 64 * kDownWaves;
-
-// Pairs and codes whose h every down workgroup quantises for itself, at most:
-// 0.8 us of each workgroup per 8192 codes, most of it while the first weights
-// are under way, against a kernel of 4.7 us (K = 7168, I = 2048: 32768 codes
-// 44.0 us against 41.8 + 4.7, 65536 codes 76.5 against 68.5 + 4.7).
-constexpr int64_t kLdsPairs = 64, kLdsCodes = 32768;
-
-// Up to this K the experts may be split over workgroups.
-constexpr int64_t kSplitMaxK = 4096;
+constexpr int kDownThreads = 64 * kDownWaves;
 
 // The S places of n float4s each into the first, in their order.
 template <int S>
@@ -724,8 +711,6 @@ __global__ __launch_bounds__(kDownThreads, 2) void k_moe_down(MoeArgs a, int cw,
   }
 }
 
-bool quant_in_down(int64_t P, int64_t I) { return P <= kLdsPairs && P * I <= kLdsCodes; }
-
 // Y from the pairs' products, 4 columns per thread, in slot order.
 template <int OUT>
 __global__ __launch_bounds__(256) void k_moe_combine(MoeArgs a) {
@@ -754,63 +739,21 @@ __global__ __launch_bounds__(256) void k_moe_combine(MoeArgs a) {
   }
 }
 
-// The down kernel's grid: columns per workgroup and workgroups per columns.
-struct DownGrid {
-  int cw, z;
-};
-
-// The fullest CU's time: its workgroups' blocks times the 128-byte lines of a
-// block (a weight row each, a row of h each, the scales) at about 4.5 ns a
-// line, and 6 us for the combine kernel where the experts are split over
-// workgroups (z > 1: few columns, many pairs; a workgroup of few columns loads
-// more of h than of the weights).  K = 256, I = 2816, 24 experts, 84 pairs:
-// 64 workgroups of 4 columns 24 us, 256 of 16 columns and a sixteenth of the
-// experts 5 us and the combine.
-DownGrid down_grid(int64_t P, int64_t most, int64_t K, int64_t IB, bool in_down) {
-  DownGrid best{16, 1};
-  double best_t = 1e30;
-  for (int z = 1; z <= (in_down || K > kSplitMaxK ? 1 : 16); z *= 2)
-    for (int cw = 32; cw >= 4; cw -= 4) {
-      const int64_t wgs = (K + cw - 1) / cw * z, blocks = (most + z - 1) / z * IB;
-      const double lines = cw + 2 + (in_down ? 0.0 : (double)P / most);
-      const double t = (double)((wgs + 255) / 256) * blocks * lines * 4.5e-3 + (z > 1 ? 6.0 : 0.0);
-      if (t < best_t) {
-        best_t = t;
-        best = {cw, z};
-      }
-    }
-  return best;
-}
-
 template <int MF, int FN, int PF, bool LDSH>
-hipError_t down_launch(const MoeArgs& a, OutKind out, DownGrid g, int most, hipStream_t st) {
-  const int P = a.T * a.topk, IB = a.I / 128;
-  const size_t res = (size_t)P * FN * 64;
-  const size_t rest = (size_t)(P * 14 + 15) / 16 * 16 +
-                      (LDSH ? (size_t)(P * IB + 3) / 4 * 16 + (size_t)P * (a.I + 16) : 0);
-  // a unit is cut for several waves only where units are few or large
-  const int cuts = 4 * P >= kDownWaves ? 4 : kDownWaves;
-  int smax = 1;
-  while (smax * 2 <= IB && smax * 2 <= cuts && smax * 2 * res + rest <= 131072) smax *= 2;
-  const dim3 grid((unsigned)((a.K + g.cw - 1) / g.cw), (unsigned)g.z), block(kDownThreads);
-  const size_t lds = smax * res + rest;
+hipError_t down_launch(const MoeArgs& a, const MoePlan& p, OutKind out, hipStream_t st) {
+  const dim3 grid((unsigned)((a.K + p.cw - 1) / p.cw), (unsigned)p.z), block(kDownThreads);
   if (out == OUT_F32)
-    hipLaunchKernelGGL((k_moe_down<MF, FN, PF, OUT_F32, LDSH>), grid, block, lds, st, a, g.cw, smax, most);
+    hipLaunchKernelGGL((k_moe_down<MF, FN, PF, OUT_F32, LDSH>), grid, block, p.down_lds, st, a, p.cw, p.smax, p.most);
   else
-    hipLaunchKernelGGL((k_moe_down<MF, FN, PF, OUT_BF16, LDSH>), grid, block, lds, st, a, g.cw, smax, most);
+    hipLaunchKernelGGL((k_moe_down<MF, FN, PF, OUT_BF16, LDSH>), grid, block, p.down_lds, st, a, p.cw, p.smax, p.most);
   return hipGetLastError();
 }
 
 template <int MFBIG, int FC, int WK>
-hipError_t gate_up_launch(const MoeArgs& a, int most, hipStream_t st) {
-  const int KB = a.K >> 7;
-  const size_t sums = (size_t)(kGuWaves / WK) * (WK - 1) * 2 * FC * MFBIG * 1024, owner = (size_t)a.E * 4;
-  const size_t scales = ((size_t)2 * KB + (size_t)16 * MFBIG * (KB | 1)) * 4;
-  size_t lds = sums > owner ? sums : owner;
-  if (scales > lds) lds = scales;
+hipError_t gate_up_launch(const MoeArgs& a, const MoePlan& p, hipStream_t st) {
   const int cols = 16 * FC * (kGuWaves / WK);
-  hipLaunchKernelGGL((k_moe_gate_up<MFBIG, FC, WK>), dim3((unsigned)(a.I / cols), (unsigned)most), dim3(kGuThreads),
-                     lds, st, a);
+  hipLaunchKernelGGL((k_moe_gate_up<MFBIG, FC, WK>), dim3((unsigned)(a.I / cols), (unsigned)p.most), dim3(kGuThreads),
+                     p.gu_lds, st, a);
   return hipGetLastError();
 }
 
@@ -828,7 +771,7 @@ int64_t moe_workspace(int64_t T, int64_t topk, int64_t I, int64_t K, MoeArgs* a,
     return p;
   };
   MoeArgs m = a ? *a : MoeArgs();
-  const bool in_down = quant_in_down(P, I);
+  const bool in_down = moe_quant_in_down(P, I);
   m.h32 = reinterpret_cast<float*>(take(P * I * 4));
   m.hq = reinterpret_cast<int8_t*>(take(in_down ? 0 : P * I));
   m.hs = reinterpret_cast<float*>(take(in_down ? 0 : P * (I / 128) * 4));
@@ -842,41 +785,25 @@ int64_t moe_workspace(int64_t T, int64_t topk, int64_t I, int64_t K, MoeArgs* a,
 }
 
 hipError_t launch_moe_block(const MoeArgs& a, OutKind out, hipStream_t st) {
-  const int P = a.T * a.topk, IB = a.I / 128;
-  const int most = P < a.E ? P : a.E;   // chosen experts, at most
-  // gate_up: experts of many rows four fragments of rows at a time, two
-  // workgroups per CU (8 experts of 64 rows: 73 us, 94 with 16 columns and
-  // three); others two fragments and four workgroups (16 to 23 rows: 52 us, 66
-  // with four fragments and 16 columns).  Columns per workgroup: 32 load the activations half as often as
-  // 16, which spread few columns more evenly (one token of 8 experts,
-  // K = 7168, I = 2048: 43 us with 32, 45 with 16; 7 experts, I = 256: 21 and
-  // 16); 64, with half the waves per column, for short K, where a workgroup's
-  // start is most of its time (K = 256, 24 experts, I = 2816: 13 us, 17, 27)
-  const int64_t w16 = (int64_t)(a.I / 16) * most, w32 = w16 / 2;
-  const bool narrow = 5 * ((w16 + 255) / 256) * 16 < 4 * ((w32 + 255) / 256) * 32;
-  hipError_t e = P > 24 * a.E                                ? gate_up_launch<4, 2, 4>(a, most, st)
-                 : a.K <= 1024 && w16 / 4 >= 512             ? gate_up_launch<2, 2, 2>(a, most, st)
-                 : narrow                                    ? gate_up_launch<2, 1, 4>(a, most, st)
-                                                             : gate_up_launch<2, 2, 4>(a, most, st);
+  const MoePlan p = moe_plan(a.T, a.topk, a.E, a.I, a.K);
+  hipError_t e = p.gu_mf == 4   ? gate_up_launch<4, 2, 4>(a, p, st)
+                 : p.gu_wk == 2 ? gate_up_launch<2, 2, 2>(a, p, st)
+                 : p.gu_fc == 1 ? gate_up_launch<2, 1, 4>(a, p, st)
+                                : gate_up_launch<2, 2, 4>(a, p, st);
   if (e != hipSuccess) return e;
-  const bool in_down = quant_in_down(P, a.I);
-  const DownGrid g = down_grid(P, most, a.K, IB, in_down);
-  const bool one = g.cw <= 16;   // one fragment of columns
-  if (in_down)
-    return one ? down_launch<1, 1, 8, true>(a, out, g, most, st) : down_launch<1, 2, 6, true>(a, out, g, most, st);
+  const bool one = p.down_fn == 1;   // one fragment of columns
+  if (p.in_down) return one ? down_launch<1, 1, 8, true>(a, p, out, st) : down_launch<1, 2, 6, true>(a, p, out, st);
+  const int P = a.T * a.topk, IB = a.I / 128;
   hipLaunchKernelGGL(k_moe_quant, dim3((unsigned)((P * IB + 31) / 32)), dim3(256), 0, st, a, P, IB);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // rows per unit by the mean rows of an expert: a unit of more rows than its
-  // expert has costs registers, one of fewer reads the weights again (32
-  // experts of 16 rows: 105 us with 32, 134 with 64)
-  if (P <= 12 * a.E)
-    e = one ? down_launch<1, 1, 8, false>(a, out, g, most, st) : down_launch<1, 2, 6, false>(a, out, g, most, st);
-  else if (P <= 28 * a.E)
-    e = one ? down_launch<2, 1, 6, false>(a, out, g, most, st) : down_launch<2, 2, 4, false>(a, out, g, most, st);
+  if (p.down_mf == 1)
+    e = one ? down_launch<1, 1, 8, false>(a, p, out, st) : down_launch<1, 2, 6, false>(a, p, out, st);
+  else if (p.down_mf == 2)
+    e = one ? down_launch<2, 1, 6, false>(a, p, out, st) : down_launch<2, 2, 4, false>(a, p, out, st);
   else
-    e = one ? down_launch<4, 1, 3, false>(a, out, g, most, st) : down_launch<4, 2, 3, false>(a, out, g, most, st);
-  if (e != hipSuccess || g.z == 1) return e;
+    e = one ? down_launch<4, 1, 3, false>(a, p, out, st) : down_launch<4, 2, 3, false>(a, p, out, st);
+  if (e != hipSuccess || p.z == 1) return e;
   const dim3 grid((unsigned)(((int64_t)a.T * (a.K / 4) + 255) / 256));
   if (out == OUT_F32)
     hipLaunchKernelGGL((k_moe_combine<OUT_F32>), grid, dim3(256), 0, st, a);
