@@ -12,10 +12,10 @@ import numpy as np
 
 # T, topk, E, I, K, ids ("spread" or "hot"), gate, down, places
 CASES = [
-    # down with its own quantiser: 2, 4 and 8 places, one and two column fragments
-    (1, 1, 1, 1024, 256, "spread", "2 1 4", "1 1 1 0", "1 8"),
-    (1, 1, 3, 1152, 384, "spread", "2 1 4", "1 1 1 0", "1 8"),
-    (1, 1, 2, 1152, 4224, "spread", "2 1 4", "1 1 2 0", "1 8"),
+    # down with its own quantiser: 1, 2 and 4 places, one and two column fragments
+    (1, 1, 1, 1024, 256, "spread", "2 1 4", "1 1 1 0", "1 4"),
+    (1, 1, 3, 1152, 384, "spread", "2 1 4", "1 1 1 0", "1 4"),
+    (1, 1, 2, 1152, 4224, "spread", "2 1 4", "1 1 2 0", "1 4"),
     (9, 3, 2, 640, 4224, "hot", "2 1 4", "1 1 2 0", "1 4"),
     (9, 3, 1, 256, 4224, "spread", "4 2 4", "1 1 2 0", "1 2"),
     (40, 1, 2, 128, 4224, "hot", "2 1 4", "1 1 2 0", "1 1"),

@@ -61,7 +61,7 @@ int main(int argc, char**) {
             CHECK(p.gu_lds + 4096 <= kCu && p.gu_lds >= (size_t)E * 4);
             CHECK(p.cw % 4 == 0 && p.cw >= 4 && p.cw <= 16 * p.down_fn);
             CHECK(p.z == 1 || (!p.in_down && K <= kSplitMaxK));
-            CHECK(p.smax == 1 || p.smax == 2 || p.smax == 4 || p.smax == 8);
+            CHECK(p.smax == 1 || p.smax == 2 || p.smax == 4);
             CHECK(p.smax <= I / 128 && p.down_lds + 256 <= kCu);
             // a lane per chosen expert and four passes of 64 groups where h is quantised in the kernel
             CHECK(!p.in_down || (P <= 64 && P * (I / 128) <= 256 && p.down_mf == 1));

@@ -673,7 +673,6 @@ __global__ __launch_bounds__(kDownThreads, 2) void k_moe_down(MoeArgs a, int cw,
   switch (smax) {
     case 2: join_places<2>(lds, P * 4 * FN); break;
     case 4: join_places<4>(lds, P * 4 * FN); break;
-    case 8: join_places<8>(lds, P * 4 * FN); break;
     default: break;
   }
   if (gridDim.y > 1) {   // k_moe_combine sums the pairs
