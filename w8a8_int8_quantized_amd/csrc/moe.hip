@@ -17,10 +17,13 @@
 // has few columns, k_moe_combine sums what several down workgroups share.
 // 64 tokens, K = 7168, I = 2048, 64 experts, 8 of them per token (2.8 GB of
 // weights, each byte fetched once by the counters): 313 + 5 + 162 us, 6.0 and
-// 5.8 TB/s; one token (352 MB): 43 + 26 us.  A "pair" is one slot of one token (t, j), p = t topk + j; the pairs of one
+// 5.8 TB/s; one token (352 MB): 43 + 26 us.
+//
+// A "pair" is one slot of one token (t, j), p = t topk + j; the pairs of one
 // expert are the rows of its products, in the order of p, and the rows of all
 // experts in the order of the expert index are the rows of hq.  A pair whose
-// id is outside 0 .. E - 1 has no row.
+// id is outside 0 .. E - 1 has no row.  Which variant of each kernel a call
+// takes stands in moe_plan.h.
 #include "common.h"
 #include "launch.h"
 #include "moe_plan.h"
@@ -283,8 +286,9 @@ __device__ __forceinline__ Chosen choose(const MoeArgs& a, int k, bool table, in
 // loads over the memory's latency, some 23 GB/s when all are at it), so the
 // kernel takes as long as the CU with the most to load (128-column
 // workgroups, one pass more than their number filled, 138 us where these take
-// 102: 8 tokens, K = 4096, I = 1536).  The 128 columns of a quantisation group may lie in
-// several workgroups; h leaves in fp32 and is quantised by its readers.
+// 102: 8 tokens, K = 4096, I = 1536).  The 128 columns of a quantisation group
+// may lie in several workgroups; h leaves in fp32 and is quantised by its
+// readers.
 template <int MF, int FC, int PF, int WK>
 __device__ __forceinline__ void gate_up_rows(const MoeArgs& a, const Chosen& c, int r0, const uint16_t* tok,
                                              float* lds) {

@@ -93,7 +93,7 @@ struct Row {
 // t + NT, ... (CH of them at most), so the row is read once and stays in
 // registers through both norms and the quantiser.  A 128-value group is the
 // 16 chunks of 16 neighbouring lanes.  HBM-bound: 4096 x 7168 with residual,
-// both norms and group codes 41 us, 206 MB at 5.0 TB/s; one row 4.5 us.
+// both norms and group codes 41 us, 206 MB at 5.0 TB/s; one row 4.4 us.
 // (The same in 64-bit arithmetic throughout takes 58 and 6.4 us, and as much
 // where only values near a border of the 16-bit type are done again in 64.)
 // LATE: all but y is loaded where it is used instead, which leaves registers
@@ -222,12 +222,21 @@ hipError_t norm_go(NormArgs a, int64_t M, hipStream_t st) {
   return hipSuccess;
 }
 
-// Few rows leave CUs idle: the row is spread as thin as it goes.  With more
-// rows fewer and fuller threads win (K = 4096: 333 rows 6.2 us with 512
-// threads x 1 chunk against 6.4 with 256 x 2, 4096 rows 23.0 against 20.6;
-// K = 8320: 1023 rows 28 us with 1024 x 2 against 17 with 512 x 3; K = 18432:
-// one row 10.1 us with 1024 x 4 against 7.4 with 1024 x 3, 1023 rows 42 us with
-// every load first against 28 LATE).
+// Up to 256 rows, one to a CU, a row is spread over more threads; with more
+// rows fewer and fuller threads win in the end.  Residual, both norms, group
+// codes, us (threads x chunks):
+//   K = 4096   64 rows 4.4 with 512 x 1, 5.1 with 256 x 2; 257 rows 5.0, 5.6;
+//              333 rows 6.0, 6.1; 1023 rows 9.6, 9.4; 4096 rows 22.2, 20.3
+//   K = 7168   64 rows 5.5 with 1024 x 1, 5.7 with 512 x 2; 257 rows 7.2, 6.9;
+//              4096 rows 49, 41
+//   K = 8320   64 rows 6.5 with 1024 x 2, 6.2 with 512 x 3; 257 rows 8.4, 8.2;
+//              1023 rows 18.6, 16.3
+//   K = 16384  64 rows 8.0 with 1024 x 2, 8.3 with 512 x 4; 1023 rows 24.6, 24.5
+//   K = 18432  one row 7.4 with 1024 x 3, 7.8 with 1024 x 4; 1023 rows 37 with
+//              every load first, 28 LATE
+// So 256 is a little early at K = 4096 and late at 8320; either costs at most
+// 0.6 us.  K <= 2048 has one shape: at 4096 rows of 512 three quarters of its
+// threads idle (11 us; 1152 12.4 us, 2048 14.3 us).
 template <bool FP16>
 hipError_t norm_launch(const NormArgs& a, int64_t M, hipStream_t st) {
   const int nch = a.K >> 3;
