@@ -417,14 +417,18 @@ int norm_residual_quant(const void* y, const void* residual, const void* post_we
 
 /*
  * The router of a mixture-of-experts layer (DeepSeek is an MoE model, page 4
- * section 1.2), in 64-bit arithmetic, so that the choice is that of the
- * formula and not of a rounding:
+ * section 1.2), in 64-bit arithmetic, so that 32-bit roundings of exp and of
+ * the sum decide no choice:
  *   s = softmax(l) or 1 / (1 + exp(-l));  c = s + bias (bias NULL: c = s)
  *   The E experts form n_group groups of E / n_group consecutive ones; a
  *   group's score is the sum of its group_top (1 or 2) largest c, and the
  *   topk_group groups of the largest score stay.  The topk experts of the
  *   largest c in them are the token's, in that order; ties go to the lower
- *   index everywhere.
+ *   index everywhere.  c is compared as rounded to 64 bits: scores that
+ *   saturate there tie whatever their logits (sigmoid: logits from about 37 up
+ *   all give 1, below about -709 all give 0; softmax: logits more than about
+ *   745 below the largest give 0; with a bias, scores below 2^-53 of it add
+ *   nothing).
  *   weight = s of the expert, over the sum of the topk s if renormalise is
  *   not 0 (0 if that sum is 0), times scale; rounded once to fp32.
  *   logits [T][E] fp32, bf16 or fp16; bias [E] fp32 or NULL

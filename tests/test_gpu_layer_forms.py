@@ -58,6 +58,20 @@ def test_route_lanes_past_the_last_expert(E, n_group):
             _check_route(logits, _route(logits, topk, **kw), topk, **kw)
 
 
+def test_route_saturated_scores_tie():
+    """Scores that 64 bits round to the same number tie, whatever their logits: the lower index, by kernel and oracle."""
+    for sigmoid, bias, logits, want in [
+            (True, None, [30.0, 38.0, 40.0, 39.0, 200.0], [1, 2, 3, 4]),
+            (True, None, [-800.0, -711.0, -30.0, -900.0], [2, 0, 1, 3]),
+            (False, None, [0.0, -750.0, -746.0, -747.0], [0, 1, 2, 3]),
+            (False, 1.0, [-40.0, -39.0, 0.0, -41.0], [2, 0, 1, 3])]:
+        l = torch.tensor([logits])
+        b = None if bias is None else torch.full((l.shape[1],), bias)
+        got = _route(l, 4, sigmoid=sigmoid, bias=b)
+        assert got[0].tolist() == [want]
+        _check_route(l, got, 4, sigmoid=sigmoid, bias=b)
+
+
 # ----------------------------------------------------------------- experts
 @pytest.mark.parametrize("case", moe_forms.CASES, ids=lambda c: "x".join(str(v) for v in c[:5]))
 def test_moe_forms(case):

@@ -9,7 +9,9 @@
 //
 // Scores and choice are computed in 64 bits: the choice is a comparison of
 // numbers that may lie anywhere near each other, and in 32 bits the rounding
-// of exp and of the sum would decide between experts whose logits differ.
+// of exp and of the sum would decide between experts whose logits differ.  In
+// 64 bits it does so only where scores saturate (sigmoid of logits from about
+// 37 up is 1): those tie, and the lower index is chosen.
 //
 // One wave per token, no barriers: expert i 64 + lane is element i of a lane,
 // so everything up to the choice is in registers.  The choice takes the
