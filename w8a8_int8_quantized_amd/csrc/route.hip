@@ -18,9 +18,10 @@
 // largest c topk times.  c is held as an unsigned integer of the same order,
 // split into two words: the largest high word is found with four DPP steps
 // and four scalar maxima, and only experts that tie in it are compared in the
-// low word.  Bound by latency and by the 64-bit exp: one token of 256 experts
-// 5.5 us, 4096 tokens 10.6 us (a workgroup per token that counted the better
-// experts for each took 10.8 and 52 us).
+// low word.  Bound by latency, and for many tokens by vector issue (832
+// instructions a token of 256 experts): one token of 256 experts 5.4 us, 4096
+// tokens 10.3 us, of which 5.9 are issue (a workgroup per token that counted the
+// better experts for each took 10.8 and 52 us).
 #include "common.h"
 #include "launch.h"
 #include "route_groups.h"
