@@ -481,6 +481,98 @@ int moe_w8a8_block(const int8_t* A, const float* a_scale, const int32_t* topk_id
                    int64_t topk, int64_t E, int64_t I, int64_t K,
                    void* workspace, int64_t workspace_bytes, void* stream);
 
+/*
+ * A key/value cache held in 4 or 8 bits, in pages of `page_size` tokens, and
+ * the attention that reads it.  Each row (one token of one key/value head, D
+ * channels) is quantised as a group of its own by the library's quantiser:
+ *   bits 8: s = fp32(max(amax, 1e-10) / 127), q in [-127, 127], one byte
+ *   bits 4: s = fp32(max(amax, 1e-10) / 7),   q in [-7, 7], nibble q + 8, the
+ *           even channel in the low nibble (as quant_weight_int4_group)
+ * so for D = 128 codes and scales are those of quant_act_group and
+ * quant_weight_int4_group on the rows, bit for bit.  A row takes Db = D bits / 8
+ * bytes.  A layer's cache is four arrays:
+ *   k_cache  [pages][Hkv][page_size][Db]
+ *   v_cache  [pages][Hkv][page_size / 4][16][4][Db / 16]: a row's channels in
+ *            sixteenths, four tokens' sixteenths next to each other (the
+ *            matrix instructions of the attention sum over tokens)
+ *   k_scale, v_scale  [pages][Hkv][page_size] fp32
+ * The slot of a token is page * page_size + its place in the page, the same for
+ * all heads.  Nothing clears a cache, and slots that no token of a call names
+ * keep their contents.
+ * D is 64, 128 or 256 (W8_ERR_SHAPE), bits 4 or 8 (W8_ERR_DTYPE), page_size a
+ * multiple of 16 up to 2^20, pages >= 1, pages * page_size < 2^31, Hkv >= 1.
+ * The four arrays are 16-byte aligned.
+ *
+ * quant_kv_cache writes rows:
+ *   k, v     [T][Hkv][D] bf16 or fp16 (dtype), k_stride and v_stride elements
+ *            from one token to the next (multiples of 8; the D channels and
+ *            the heads are contiguous), so parts of one projection's output
+ *            can be passed as they lie
+ *   slots    [T] int32 DEVICE array; a slot outside 0 .. pages * page_size - 1
+ *            (a padding token) writes nothing.  Slots are distinct: of two
+ *            tokens with one slot, that slot holds an unspecified mixture.
+ * dequant_kv_cache reads rows back, out[t] = q * s in fp32, rounded once:
+ *   k, v     [T][Hkv][D] out, bf16, fp16 or fp32 (dtype), contiguous; tokens
+ *            whose slot lies outside give zeros.  Slots may repeat.
+ * T * Hkv <= 2^27.
+ */
+int quant_kv_cache(const void* k, const void* v, int dtype, int64_t k_stride,
+                   int64_t v_stride, const int32_t* slots, int64_t T, int64_t Hkv,
+                   int64_t D, int bits, int64_t pages, int64_t page_size,
+                   void* k_cache, float* k_scale, void* v_cache, float* v_scale,
+                   void* stream);
+
+int dequant_kv_cache(const void* k_cache, const float* k_scale, const void* v_cache,
+                     const float* v_scale, const int32_t* slots, int64_t T,
+                     int64_t Hkv, int64_t D, int bits, int64_t pages,
+                     int64_t page_size, void* k, void* v, int dtype, void* stream);
+
+/*
+ * Attention of B sequences' query tokens over the cache above.  Sequence b has
+ * L = kv_lens[b] cached tokens, its newest n among them the query tokens'
+ * own (written by quant_kv_cache before this call), in the pages
+ * block_table[b][0 .. ceil(L / page_size) - 1].  Query head j reads key/value
+ * head j / (Hq / Hkv):
+ *   s[t] = scale * sum_d q[d] * k[t][d],  p = exp(s - max s)
+ *   out  = sum_t p[t] v[t] / sum_t p[t],  lse = ln sum_t exp(s[t])
+ * over the tokens t that the query sees: with causal, query i of n sees
+ * t <= L - n + i; without, all L.  A query that sees nothing (L = 0, or more
+ * queries than cached tokens) gives zeros and lse -inf.
+ *   q        [T][Hq][D] bf16 or fp16 (dtype), q_stride elements from one token
+ *            to the next (a multiple of 8; heads and channels contiguous)
+ *   block_table [B][max_pages] int32, kv_lens [B] int32: DEVICE arrays.
+ *            Entries behind a sequence's last page are not read.
+ *   q_starts [B+1] int32 DEVICE array: sequence b's query tokens are rows
+ *            q_starts[b] .. q_starts[b+1] - 1, max_q of them at most.  NULL:
+ *            max_q tokens each, T == B * max_q.  Rows of no sequence are
+ *            left untouched.
+ *   out      [T][Hq][D] of q's type; lse [T][Hq] fp32 or NULL
+ *   workspace: caller-owned device memory of attn_workspace_bytes(max_q, Hq,
+ *            Hkv, D) bytes (fewer gives W8_ERR_WORKSPACE), 256-byte aligned,
+ *            with no contents to keep; it must not be used by other work
+ *            until the stream has passed this call, so calls on different
+ *            streams, or graphs that may run at the same time, need one each.
+ * Scores, exponentials and sums are fp32; q enters exactly; p times the value
+ * scale is rounded to fp16 (relative to the largest so far) for the second
+ * product; out is rounded once.  Codes and scales behind a sequence's last
+ * token may be anything, NaN among it.  Lengths and starts that contradict the
+ * sizes are clamped to them, and table entries outside 0 .. pages - 1 read as
+ * some page: unspecified values, no out-of-bounds access.
+ * Hq is a multiple of Hkv, Hq <= 4096; max_q <= T;
+ * B Hkv ceil(max_q Hq / Hkv / 16) ceil(max_pages page_size / 32) < 2^31.
+ * Nothing is allocated; the call can be captured into a graph.
+ */
+int64_t attn_workspace_bytes(int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D);
+
+int attn_kv_cache(const void* q, int dtype, int64_t q_stride, const void* k_cache,
+                  const float* k_scale, const void* v_cache, const float* v_scale,
+                  const int32_t* block_table, const int32_t* kv_lens,
+                  const int32_t* q_starts, int64_t B, int64_t T, int64_t max_q,
+                  int64_t Hq, int64_t Hkv, int64_t D, int bits, int64_t pages,
+                  int64_t page_size, int64_t max_pages, float scale, int causal,
+                  void* out, float* lse, void* workspace, int64_t workspace_bytes,
+                  void* stream);
+
 #ifdef __cplusplus
 }
 #endif

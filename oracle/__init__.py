@@ -35,6 +35,7 @@ Modules:
   asym     - the asymmetric uint8 activation variant
   int4     - group-wise INT4 weights (packed two per byte) and the W4A16 GEMM
   layer    - the norms with residual and gate, the router, the few-token experts
+  cache    - a key/value cache in 4 or 8 bits and the attention over it
 """
 
-from . import formats, quant, gemm, routing, int4, layer  # noqa: F401
+from . import formats, quant, gemm, routing, int4, layer, cache  # noqa: F401

@@ -17,6 +17,9 @@ fallback: if libw8a8.so is missing, importing this package raises.
     h, q, s, z = norm_residual_quant(y, w, residual=r, normed=True)   # norms, residual and quantiser in one pass
     ids, wt = moe_route_topk(logits, 8)        # the experts of each token and their weights
     y = moe_w8a8_block(q, s, ids, wt, w_gu, s_gu, w_dn, s_dn)   # all their products, up to 64 tokens
+    cache = kv_cache_empty(pages, kv_heads, 64, 128, bits=4)    # a layer's key/value cache in 4 (or 8) bits
+    quant_kv_cache(k, v, slots, cache)                          # new tokens' rows into their slots
+    o = attn_kv_cache(q, cache, block_table, kv_lens)           # attention over it
 """
 
 import ctypes
@@ -97,6 +100,14 @@ _FUNCS = {
     "moe_route_topk": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_int]
                        + [ctypes.c_int64] * 6 + [ctypes.c_int, ctypes.c_double] + [ctypes.c_void_p] * 3),
     "moe_workspace_bytes": (ctypes.c_int64, [ctypes.c_int64] * 4),
+    "quant_kv_cache": (ctypes.c_int, [ctypes.c_void_p] * 2 + [ctypes.c_int] + [ctypes.c_int64] * 2 + [ctypes.c_void_p]
+                       + [ctypes.c_int64] * 3 + [ctypes.c_int] + [ctypes.c_int64] * 2 + [ctypes.c_void_p] * 5),
+    "dequant_kv_cache": (ctypes.c_int, [ctypes.c_void_p] * 5 + [ctypes.c_int64] * 3 + [ctypes.c_int]
+                         + [ctypes.c_int64] * 2 + [ctypes.c_void_p] * 2 + [ctypes.c_int, ctypes.c_void_p]),
+    "attn_workspace_bytes": (ctypes.c_int64, [ctypes.c_int64] * 4),
+    "attn_kv_cache": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64] + [ctypes.c_void_p] * 7
+                      + [ctypes.c_int64] * 6 + [ctypes.c_int] + [ctypes.c_int64] * 3 + [ctypes.c_float, ctypes.c_int]
+                      + [ctypes.c_void_p] * 3 + [ctypes.c_int64, ctypes.c_void_p]),
     "moe_w8a8_block": (ctypes.c_int, [ctypes.c_void_p] * 9 + [ctypes.c_int] + [ctypes.c_int64] * 5
                        + [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
 }
@@ -602,4 +613,154 @@ def moe_w8a8_block(A, a_scale, topk_ids, topk_weights, W_gate_up, gate_up_scale,
             topk_weights.data_ptr(), W_gate_up.data_ptr(), gate_up_scale.data_ptr(), W_down.data_ptr(),
             down_scale.data_ptr(), out.data_ptr(), W8_FP32 if out.dtype == torch.float32 else W8_BF16, T, topk, E, I,
             K, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return out
+
+
+# ------------------------------------------------- a quantised key/value cache
+def kv_cache_empty(pages, kv_heads, page_size, head_dim, bits=4, device="cuda"):
+    """The arrays of a layer's key/value cache, uninitialised: (k, k_scale, v, v_scale).
+
+    k [pages, kv_heads, page_size, Db] and v [pages, kv_heads, page_size / 4,
+    16, 4, Db / 16], Db = head_dim * bits / 8, uint8 for 4 bits (two nibbles
+    q + 8 a byte) and int8 for 8; k_scale and v_scale [pages, kv_heads,
+    page_size] fp32.  The slot of a token is page * page_size + its place in
+    the page.
+    """
+    if bits not in (4, 8) or head_dim not in (64, 128, 256) or page_size < 16 or page_size % 16:
+        raise W8Error("kv_cache_empty: bits must be 4 or 8, head_dim 64, 128 or 256, page_size a multiple of 16, got "
+                      f"{bits}, {head_dim}, {page_size}")
+    db, dt = head_dim * bits // 8, torch.uint8 if bits == 4 else torch.int8
+    return (torch.empty(pages, kv_heads, page_size, db, dtype=dt, device=device),
+            torch.empty(pages, kv_heads, page_size, dtype=torch.float32, device=device),
+            torch.empty(pages, kv_heads, page_size // 4, 16, 4, db // 16, dtype=dt, device=device),
+            torch.empty(pages, kv_heads, page_size, dtype=torch.float32, device=device))
+
+
+def _kv_cache(cache):
+    """A cache's (bits, head_dim, pages, heads, page size, device), its arrays checked against each other."""
+    k, ks, v, vs = cache
+    _dev(k)
+    _dims(k, "cache k", 4)
+    if k.dtype not in (torch.uint8, torch.int8):
+        raise W8Error(f"cache k must be uint8 (4 bits) or int8 (8 bits), got {k.dtype}")
+    pages, H, page, db = k.shape
+    dev = k.device
+    _like(ks, "cache k_scale", (pages, H, page), torch.float32, dev)
+    _like(v, "cache v", (pages, H, page // 4, 16, 4, db // 16), k.dtype, dev)
+    _like(vs, "cache v_scale", (pages, H, page), torch.float32, dev)
+    bits = 4 if k.dtype == torch.uint8 else 8
+    return bits, db * 8 // bits, pages, H, page, dev
+
+
+def _token_rows(t, name, shape, dtype, dev):
+    """The stride between tokens of t [T, heads, D], whose heads and channels are contiguous."""
+    if t.shape != shape or t.dtype != dtype or t.device != dev:
+        raise W8Error(f"{name} must be {dtype} {shape} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    T, H, D = shape
+    if t.numel() and (t.stride(2) != 1 or (H > 1 and t.stride(1) != D)):
+        raise W8Error(f"{name}: heads and channels must be contiguous")
+    return t.stride(0) if T > 1 else H * D
+
+
+def quant_kv_cache(k, v, slots, cache):
+    """Quantises the rows of k and v [T, kv_heads, D] (bf16 or fp16) into the
+    slots int32 [T] of a cache (kv_cache_empty), one scale per token and head.
+
+    k and v may be strided between tokens (parts of one projection's output).
+    Slots are distinct; a token whose slot is negative or past the cache
+    writes nothing.
+    """
+    bits, D, pages, H, page, dev = _kv_cache(cache)
+    _dims(k, "k", 3)
+    T = k.shape[0]
+    k_stride = _token_rows(k, "k", (T, H, D), k.dtype, dev)
+    v_stride = _token_rows(v, "v", (T, H, D), k.dtype, dev)
+    _like(slots, "slots", (T,), torch.int32, dev)
+    kc, ks, vc, vs = cache
+    _run_on(dev, "quant_kv_cache", lib.quant_kv_cache, k.data_ptr(), v.data_ptr(), _act_dtype(k), k_stride, v_stride,
+            slots.data_ptr(), T, H, D, bits, pages, page, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr())
+
+
+def dequant_kv_cache(cache, slots, dtype=torch.bfloat16, out=None):
+    """The keys and values [T, kv_heads, D] (bf16, fp16 or fp32) of a cache's
+    slots int32 [T]: code times scale, rounded once; zeros for a slot that is
+    negative or past the cache.  out: an optional (k, v) pair to write."""
+    bits, D, pages, H, page, dev = _kv_cache(cache)
+    _dims(slots, "slots", 1)
+    T = slots.shape[0]
+    _like(slots, "slots", (T,), torch.int32, dev)
+    if out is None:
+        out = torch.empty(T, H, D, dtype=dtype, device=dev), torch.empty(T, H, D, dtype=dtype, device=dev)
+    else:
+        dtype = out[0].dtype
+        _like(out[0], "out k", (T, H, D), dtype, dev)
+        _like(out[1], "out v", (T, H, D), dtype, dev)
+    code = W8_FP32 if dtype == torch.float32 else _act_dtype(out[0])
+    kc, ks, vc, vs = cache
+    _run_on(dev, "dequant_kv_cache", lib.dequant_kv_cache, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(),
+            slots.data_ptr(), T, H, D, bits, pages, page, out[0].data_ptr(), out[1].data_ptr(), code)
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def attn_workspace_bytes(max_q, q_heads, kv_heads, head_dim):
+    """Bytes of workspace attn_kv_cache needs."""
+    n = lib.attn_workspace_bytes(max_q, q_heads, kv_heads, head_dim)
+    _check(min(n, 0), "attn_workspace_bytes")
+    return n
+
+
+def attn_kv_cache(q, cache, block_table, kv_lens, q_starts=None, max_q=None, scale=None, causal=True, lse=False,
+                  out=None, workspace=None):
+    """Attention of the query tokens q [T, Hq, D] (bf16 or fp16) over a quantised
+    cache (kv_cache_empty): out [T, Hq, D], or (out, lse fp32 [T, Hq]) with lse=True.
+
+    Sequence b has kv_lens[b] cached tokens (int32 [B], its query tokens' own
+    among them) in the pages block_table[b] (int32 [B, max_pages]).  Without
+    q_starts every sequence has T / B query tokens; with q_starts int32 [B + 1]
+    sequence b has the rows q_starts[b] .. q_starts[b + 1] - 1, max_q of them at
+    most (default T), and rows of no sequence are left as they were.  causal:
+    query i of n sees the first kv_lens[b] - n + i + 1 tokens, otherwise all; one
+    that sees none gives zeros and lse -inf.  scale: D ** -0.5 by default.
+    Hq is a multiple of the cache's heads, whose query heads are neighbours.
+    out: the tensor to write, or (out, lse) with lse=True.  workspace: uint8,
+    attn_workspace_bytes(max_q, Hq, kv_heads, D) or more; without one, torch
+    allocates it for the call.
+    """
+    bits, D, pages, H, page, dev = _kv_cache(cache)
+    _dims(q, "q", 3)
+    T, Hq = q.shape[0], q.shape[1]
+    code = _act_dtype(q)
+    stride = _token_rows(q, "q", (T, Hq, D), q.dtype, dev)
+    _dims(block_table, "block_table", 2)
+    B, max_pages = block_table.shape
+    _like(block_table, "block_table", (B, max_pages), torch.int32, dev)
+    _like(kv_lens, "kv_lens", (B,), torch.int32, dev)
+    if q_starts is not None:
+        _like(q_starts, "q_starts", (B + 1,), torch.int32, dev)
+        max_q = T if max_q is None else min(max_q, T)
+    else:
+        n = T // B if B else 0
+        if n * B != T or max_q not in (None, n):
+            raise W8Error(f"attn_kv_cache: {T} query tokens for {B} sequences without q_starts")
+        max_q = n
+    if Hq % H or not Hq:
+        raise W8Error(f"attn_kv_cache: {Hq} query heads for {H} key/value heads")
+    if out is None:
+        out = torch.empty(T, Hq, D, dtype=q.dtype, device=dev)
+        if lse:
+            out = out, torch.empty(T, Hq, dtype=torch.float32, device=dev)
+    elif lse:
+        _like(out[1], "out lse", (T, Hq), torch.float32, dev)
+    o, z = out if lse else (out, None)
+    _like(o, "out", (T, Hq, D), q.dtype, dev)
+    if workspace is None:
+        workspace = torch.empty(attn_workspace_bytes(max_q, Hq, H, D), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise W8Error(f"workspace must be contiguous, on {dev}")
+    kc, ks, vc, vs = cache
+    _run_on(dev, "attn_kv_cache", lib.attn_kv_cache, q.data_ptr(), code, stride, kc.data_ptr(), ks.data_ptr(),
+            vc.data_ptr(), vs.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), _ptr(q_starts), B, T, max_q, Hq,
+            H, D, bits, pages, page, max_pages, D ** -0.5 if scale is None else scale, causal, o.data_ptr(), _ptr(z),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out

@@ -477,4 +477,144 @@ int moe_w8a8_block(const int8_t* A, const float* a_scale, const int32_t* topk_id
   return status_of(w8::launch_moe_block(a, out, as_stream(stream)));
 }
 
+// The rules of a quantised cache, shared by the calls on it.
+static int check_kv(int64_t Hkv, int64_t D, int bits, int64_t pages, int64_t page_size) {
+  if (bits != 4 && bits != 8) return W8_ERR_DTYPE;
+  if (D != 64 && D != 128 && D != 256) return W8_ERR_SHAPE;
+  if (Hkv < 1 || Hkv > w8::kKvMaxHeads || pages < 1 || pages > kMaxRows) return W8_ERR_SHAPE;
+  if (page_size < 16 || page_size > w8::kKvMaxPage || (page_size & 15) != 0) return W8_ERR_SHAPE;
+  return pages * page_size > kMaxRows ? W8_ERR_SHAPE : W8_OK;
+}
+
+static int check_kv_pointers(const void* k, const float* ks, const void* v, const float* vs) {
+  if (!k || !ks || !v || !vs) return W8_ERR_NULL;
+  return aligned(k, 16) && aligned(ks, 16) && aligned(v, 16) && aligned(vs, 16) ? W8_OK : W8_ERR_ALIGN;
+}
+
+// A stride between tokens whose rows are read 16 bytes at a time.
+static bool token_stride(int64_t s) { return s >= 0 && (s & 7) == 0 && s < kMaxElems; }
+
+static w8::KvArgs kv_args(const void* k, const float* ks, const void* v, const float* vs, const int32_t* slots,
+                          int64_t T, int64_t H, int64_t pages, int64_t page_size) {
+  w8::KvArgs a = {};
+  a.slots = slots;
+  a.k = static_cast<uint8_t*>(const_cast<void*>(k));
+  a.v = static_cast<uint8_t*>(const_cast<void*>(v));
+  a.ks = const_cast<float*>(ks);
+  a.vs = const_cast<float*>(vs);
+  a.T = T;
+  a.H = H;
+  a.page = (int)page_size;
+  a.slots_end = (int)(pages * page_size);
+  return a;
+}
+
+int quant_kv_cache(const void* k, const void* v, int dtype, int64_t k_stride, int64_t v_stride, const int32_t* slots,
+                   int64_t T, int64_t Hkv, int64_t D, int bits, int64_t pages, int64_t page_size, void* k_cache,
+                   float* k_scale, void* v_cache, float* v_scale, void* stream) {
+  if (dtype != W8_BF16 && dtype != W8_FP16) return W8_ERR_DTYPE;
+  int rc = check_kv(Hkv, D, bits, pages, page_size);
+  if (rc) return rc;
+  if (T < 0 || T > w8::kKvMaxRows / Hkv || !token_stride(k_stride) || !token_stride(v_stride)) return W8_ERR_SHAPE;
+  if (T == 0) return W8_OK;
+  if (!k || !v || !slots) return W8_ERR_NULL;
+  rc = check_kv_pointers(k_cache, k_scale, v_cache, v_scale);
+  if (rc) return rc;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4)) return W8_ERR_ALIGN;
+  w8::KvArgs a = kv_args(k_cache, k_scale, v_cache, v_scale, slots, T, Hkv, pages, page_size);
+  a.k16 = k;
+  a.v16 = v;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  return status_of(w8::launch_kv(a, true, dtype, bits, (int)D, as_stream(stream)));
+}
+
+int dequant_kv_cache(const void* k_cache, const float* k_scale, const void* v_cache, const float* v_scale,
+                     const int32_t* slots, int64_t T, int64_t Hkv, int64_t D, int bits, int64_t pages,
+                     int64_t page_size, void* k, void* v, int dtype, void* stream) {
+  if (dtype != W8_BF16 && dtype != W8_FP16 && dtype != W8_FP32) return W8_ERR_DTYPE;
+  int rc = check_kv(Hkv, D, bits, pages, page_size);
+  if (rc) return rc;
+  if (T < 0 || T > w8::kKvMaxRows / Hkv) return W8_ERR_SHAPE;
+  if (T == 0) return W8_OK;
+  if (!k || !v || !slots) return W8_ERR_NULL;
+  rc = check_kv_pointers(k_cache, k_scale, v_cache, v_scale);
+  if (rc) return rc;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4)) return W8_ERR_ALIGN;
+  w8::KvArgs a = kv_args(k_cache, k_scale, v_cache, v_scale, slots, T, Hkv, pages, page_size);
+  a.k_out = k;
+  a.v_out = v;
+  return status_of(w8::launch_kv(a, false, dtype, bits, (int)D, as_stream(stream)));
+}
+
+// The head and size rules of the attention, shared by the call and its workspace query.
+static int check_attn(int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D) {
+  if (D != 64 && D != 128 && D != 256) return W8_ERR_SHAPE;
+  if (Hkv < 1 || Hkv > w8::kKvMaxHeads || Hq < Hkv || Hq > w8::kKvMaxHeads || Hq % Hkv != 0) return W8_ERR_SHAPE;
+  return max_q < 0 || max_q > kMaxRows / Hq ? W8_ERR_SHAPE : W8_OK;
+}
+
+int64_t attn_workspace_bytes(int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D) {
+  int rc = check_attn(max_q, Hq, Hkv, D);
+  if (rc) return rc;
+  w8::AttnArgs a = {};
+  a.sh.max_q = (int)max_q;
+  a.sh.G = (int)(Hq / Hkv);
+  return w8::attn_workspace(&a, D, nullptr);
+}
+
+int attn_kv_cache(const void* q, int dtype, int64_t q_stride, const void* k_cache, const float* k_scale,
+                  const void* v_cache, const float* v_scale, const int32_t* block_table, const int32_t* kv_lens,
+                  const int32_t* q_starts, int64_t B, int64_t T, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D,
+                  int bits, int64_t pages, int64_t page_size, int64_t max_pages, float scale, int causal, void* out,
+                  float* lse, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (dtype != W8_BF16 && dtype != W8_FP16) return W8_ERR_DTYPE;
+  int rc = check_kv(Hkv, D, bits, pages, page_size);
+  if (rc) return rc;
+  rc = check_attn(max_q, Hq, Hkv, D);
+  if (rc) return rc;
+  if (B < 0 || B > kMaxRows || T < 0 || T > kMaxRows / Hq || max_q > T || max_pages < 0 || max_pages > kMaxRows)
+    return W8_ERR_SHAPE;
+  if (!token_stride(q_stride)) return W8_ERR_SHAPE;
+  if (!q_starts && T != B * max_q) return W8_ERR_SHAPE;
+  if (max_pages * page_size > kMaxRows) return W8_ERR_SHAPE;
+  // written so that a NaN fails
+  if (!(scale >= -3.4e38f && scale <= 3.4e38f)) return W8_ERR_VALUE;
+  if (B == 0 || T == 0 || max_q == 0) return W8_OK;
+  // the units of work stay inside 32 bits whatever the arrays hold
+  const int64_t row_tiles = (max_q * (Hq / Hkv) + 15) / 16, tiles = (max_pages * page_size + 31) / 32 + 1;
+  if (B > kMaxRows / Hkv || B * Hkv > kMaxRows / row_tiles || B * Hkv * row_tiles > kMaxRows / tiles)
+    return W8_ERR_SHAPE;
+  if (!q || !kv_lens || !out || !workspace || (max_pages > 0 && !block_table)) return W8_ERR_NULL;
+  rc = check_kv_pointers(k_cache, k_scale, v_cache, v_scale);
+  if (rc) return rc;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(block_table, 4) || !aligned(kv_lens, 4) ||
+      !aligned(q_starts, 4) || !aligned(workspace, 256))
+    return W8_ERR_ALIGN;
+  w8::AttnArgs a = {};
+  a.q = q;
+  a.q_stride = q_stride;
+  a.k = static_cast<const uint8_t*>(k_cache);
+  a.v = static_cast<const uint8_t*>(v_cache);
+  a.ks = k_scale;
+  a.vs = v_scale;
+  a.table = block_table;
+  a.kv_lens = kv_lens;
+  a.q_starts = q_starts;
+  a.out = out;
+  a.lse = lse;
+  a.sh.B = (int)B;
+  a.sh.T = (int)T;
+  a.sh.Hkv = (int)Hkv;
+  a.sh.G = (int)(Hq / Hkv);
+  a.sh.max_q = (int)max_q;
+  a.sh.page = (int)page_size;
+  a.sh.max_pages = (int)max_pages;
+  a.sh.causal = causal != 0;
+  a.pages = (int)pages;
+  a.scale_log2 = (float)(scale * 1.4426950408889634);
+  if (workspace_bytes < w8::attn_workspace(&a, D, workspace)) return W8_ERR_WORKSPACE;
+  return status_of(w8::launch_attn(a, dtype == W8_FP16, bits, (int)D, as_stream(stream)));
+}
+
 }  // extern "C"

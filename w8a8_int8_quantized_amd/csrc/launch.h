@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "attn_plan.h"
 #include "workspace.h"
 
 namespace w8 {
@@ -119,6 +120,39 @@ struct MoeArgs {
 int64_t moe_workspace(int64_t T, int64_t topk, int64_t I, int64_t K, MoeArgs* a, void* ws);
 hipError_t launch_moe_block(const MoeArgs& a, OutKind out, hipStream_t st);
 constexpr int64_t kMoeMaxT = 64, kMoeMaxTopk = 16, kMoeMaxSide = 1 << 15, kMoeMaxE = 4096;
+
+// Keys and values into and out of a quantised cache (kvcache.hip); dtype of a
+// launch: a w8_dtype.
+struct KvArgs {
+  const void *k16, *v16;          // written from: [T][H][D] rows, stride elements between tokens
+  int64_t k_stride, v_stride;
+  void *k_out, *v_out;            // read to
+  const int32_t* slots;
+  uint8_t *k, *v;
+  float *ks, *vs;
+  int64_t T, H, T4;               // T4: set by the launcher
+  int page, slots_end;            // slots_end: pages * page
+};
+constexpr int64_t kKvMaxHeads = 4096, kKvMaxPage = 1 << 20, kKvMaxRows = 1 << 27;   // rows: T * H
+hipError_t launch_kv(KvArgs a, bool write, int dtype, int bits, int D, hipStream_t st);
+
+// Attention over that cache (attn.hip); q_starts and lse may be null.
+// attn_workspace gives the workspace's size from a->sh and sets what depends
+// on it (part and part_ml in ws, the row tile, the grid).
+struct AttnArgs {
+  const void* q;
+  int64_t q_stride;
+  const uint8_t *k, *v;
+  const float *ks, *vs;
+  const int32_t *table, *kv_lens, *q_starts;
+  void* out;
+  float *lse, *part, *part_ml;
+  AttnShape sh;
+  int pages, workgroups;
+  float scale_log2;               // scale * log2(e)
+};
+int64_t attn_workspace(AttnArgs* a, int64_t D, void* ws);
+hipError_t launch_attn(const AttnArgs& a, bool fp16, int bits, int D, hipStream_t st);
 
 // The library's own scratch (rules in workspace.h): at least `bytes` of
 // device memory for (current device, `st`, `slot`), slot 0 for split-K
