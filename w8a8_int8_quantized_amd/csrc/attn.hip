@@ -16,7 +16,12 @@
 // quarter of a token's channels.  Values lie in blocks of four tokens by
 // sixteenths of the channels (include/w8a8.h): a lane reads its four tokens'
 // sixteenth, and bytes of two tokens are joined by one byte permutation.
-// No operand passes through LDS.
+//
+// Each wave streams its tiles through a ring of its own in LDS, filled by
+// direct-to-LDS loads that read memory in order: no registers and no barriers,
+// and a load is in flight while the tiles before it are computed.  Keys are
+// swizzled within a row on the way, so that the fragment reads meet no bank
+// conflicts.
 //
 // Codes to 16-bit floats: OR an exponent on top of the code bits in place,
 // which gives 2^k + code + offset exactly.  For the keys the constant is not
@@ -25,12 +30,12 @@
 // fp16): a running sum over a long cache must not carry an offset that is
 // larger than its result.
 //
-// Softmax: m is a reference that a row's scores may pass by a factor of 32
-// before it moves (the largest p vs / vref is looked at, one compare a tile),
-// so the accumulators are seldom rescaled.  p vs goes into the second product
-// as fp16, scaled by 1024 / vref (vref: the largest vs so far): half a step is
-// 2^-11 of the probability, and what lies 2^-24 below the largest term is
-// rounded to that.  m, l and all sums are fp32.
+// Softmax: a row's probabilities are exp2(s - m) with a reference m that the
+// largest term p vs passes by 2^10 to 2^15 before it moves (one compare a
+// tile), so the accumulators are seldom rescaled.  p vs goes into the second
+// product as fp16: half a step is 2^-11 of the term, and what lies 2^-24 below
+// the largest is rounded to that.  References, l and all sums are fp32; the
+// reference cancels in o = O / l.
 //
 // Work is shared out in equal runs of 32-token tiles over all sequences and
 // heads (attn_plan.h); the waves of a workgroup take parts of a segment's run
@@ -39,6 +44,7 @@
 #include "attn_plan.h"
 #include "common.h"
 #include "launch.h"
+#include "pipeline.h"
 
 namespace w8 {
 namespace {
@@ -50,41 +56,82 @@ typedef float v2f __attribute__((ext_vector_type(2)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
-constexpr float kUnset = -1e30f;     // a reference before the first score
-constexpr float kLift = 1024.f;      // what the largest p vs / vref is scaled to
-constexpr float kLimit = 32768.f;    // and what it may grow to: fp16 ends at 65504
+constexpr float kUnset = -1e30f;          // a reference before the first score
+constexpr float kLift = 10.f;             // log2 of what the largest p vs becomes
+constexpr float kTermLimit = 32768.f;     // what p vs may grow to: fp16 ends at 65504
+constexpr float kSumLimit = 1.2676506e30f;   // what a sum of p may grow to within a tile, 2^100
+constexpr float kTinyScale = 5.9604645e-8f;  // 2^-24: a value scale counts as this at least in the reference
 constexpr float kLn2 = 0.693147180559945309f;
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Across the four lanes of a row (lane ^ 16, lane ^ 32).
-__device__ __forceinline__ float row_max(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16, 64));
-  return fmaxf(v, __shfl_xor(v, 32, 64));
-}
-__device__ __forceinline__ float row_sum(float v) {
-  v += __shfl_xor(v, 16, 64);
-  return v + __shfl_xor(v, 32, 64);
+// ln(l 2^m): the exponents are added exactly before the logarithm's rounding.
+__device__ __forceinline__ float log_sum(float m, float l) {
+  const float e = (float)__builtin_amdgcn_frexp_expf(l);
+  return l > 0.f ? kLn2 * ((m + e) + __log2f(__builtin_amdgcn_frexp_mantf(l))) : -__builtin_inff();
 }
 
-// N dwords of a lane from a 4 N-byte aligned address.
-template <int N>
-__device__ __forceinline__ void load_words(uint32_t* w, const uint8_t* p) {
-  if constexpr (N >= 4) {
+// Across the lanes of a row: lane ^ FROM, lane ^ 2 FROM, .. lane ^ 32.
+template <int FROM>
+__device__ __forceinline__ float row_max(float v) {
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const v4u v = *reinterpret_cast<const v4u*>(p + 16 * i);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[4 * i + j] = v[j];
-    }
-  } else {
-    const v2u v = *reinterpret_cast<const v2u*>(p);
-    w[0] = v[0];
-    w[1] = v[1];
-  }
+  for (int d = FROM; d < 64; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+  return v;
 }
+template <int FROM>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int d = FROM; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+
+// `to`, with the lanes of bank B (4 B .. 4 B + 3 of each 16) taken from x, SH
+// lanes below.
+template <int SH, int BANKS>
+__device__ __forceinline__ float from_below(float to, float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(to), __float_as_int(x), 0x110 + SH, 0xF, BANKS, false));
+}
+// x of the lane SH above within the 16 (0 past the end).
+template <int SH>
+__device__ __forceinline__ uint32_t from_above(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x100 + SH, 0xF, 0xF, true);
+}
+
+// 16 bytes per lane from base + voff into LDS at lds + 16 lane, and 4 bytes per
+// lane from an address of its own into lds + 4 lane.  No register result, so
+// nothing can be overwritten while a load is in flight; the caller counts them.
+// (The wait states: M0 and the base may have been written just before.)
+__device__ __forceinline__ void dma_rows(const uint8_t* base, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
+               ::"s"(lds), "v"(voff), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void dma_rows_at(const uint8_t* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off"
+               ::"s"(lds), "v"(p) : "memory", "m0");
+}
+__device__ __forceinline__ void dma_word_at(const uint8_t* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, off"
+               ::"s"(lds), "v"(p) : "memory", "m0");
+}
+// All but N of the wave's vector memory operations are done; its LDS reads are.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void wait_lds_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 // ------------------------------------------------------------ codes to floats
+// (x & mask) | exponent in one instruction: one operand of v_and_or_b32 can be
+// a constant, so the exponents stay in registers that the compiler is kept from
+// seeing through.
+__device__ __forceinline__ uint32_t held(uint32_t c) {
+  asm("" : "+v"(c));
+  return c;
+}
+struct Exponents {
+  uint32_t key, lo, hi;           // of the key codes, and of the low and high nibbles (or bytes) of values
+};
+
 // The key operand of one matrix instruction, 8 channels of a lane's quarter.
 // 4 bits: channels in the order 0 4 1 5 2 6 3 7 (the query's operand has the
 // same), value 128 + n (bf16) or 64 + n (fp16), n = code + 8.  8 bits: in
@@ -92,23 +139,24 @@ __device__ __forceinline__ void load_words(uint32_t* w, const uint8_t* p) {
 template <bool FP16, int BITS>
 struct KeyCodes {
   static constexpr float kOffset = BITS == 4 ? (FP16 ? 72.f : 136.f) : (FP16 ? 1152.f : 128.f);
-  static __device__ __forceinline__ v4u operand(const uint32_t* w) {
+  static constexpr uint32_t kExp = BITS == 4 ? (FP16 ? 0x54005400u : 0x43004300u) : 0x64646464u;
+  static __device__ __forceinline__ v4u operand(const uint32_t* w, uint32_t e) {
     v4u r;
     if constexpr (BITS == 4 && FP16) {
-      r[0] = ((w[0] << 4) & 0x00F000F0u) | 0x54005400u;
-      r[1] = (w[0] & 0x00F000F0u) | 0x54005400u;
-      r[2] = ((w[0] >> 4) & 0x00F000F0u) | 0x54005400u;
-      r[3] = ((w[0] >> 8) & 0x00F000F0u) | 0x54005400u;
+      r[0] = ((w[0] << 4) & 0x00F000F0u) | e;
+      r[1] = (w[0] & 0x00F000F0u) | e;
+      r[2] = ((w[0] >> 4) & 0x00F000F0u) | e;
+      r[3] = ((w[0] >> 8) & 0x00F000F0u) | e;
     } else if constexpr (BITS == 4) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = ((w[0] >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+      for (int i = 0; i < 4; ++i) r[i] = ((w[0] >> (4 * i)) & 0x000F000Fu) | e;
     } else {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t u = w[i] ^ 0x80808080u;
         if constexpr (FP16) {
-          r[2 * i] = __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u);
-          r[2 * i + 1] = __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u);
+          r[2 * i] = __builtin_amdgcn_perm(e, u, 0x04010400u);
+          r[2 * i + 1] = __builtin_amdgcn_perm(e, u, 0x04030402u);
         } else {
           const uint32_t f0 = __float_as_uint((float)(u & 0xffu)), f1 = __float_as_uint((float)((u >> 8) & 0xffu));
           const uint32_t f2 = __float_as_uint((float)((u >> 16) & 0xffu)), f3 = __float_as_uint((float)(u >> 24));
@@ -136,25 +184,39 @@ __device__ __forceinline__ uint32_t less(uint32_t h, float by) {
 }
 
 // --------------------------------------------------------------- one segment
-template <bool FP16, int D, int BITS, int R>
+template <bool FP16, int D, int BITS, int ROWS>
 struct Attn {
+  static constexpr int R = ROWS > 16 ? ROWS / 16 : 1;      // row fragments of 16 columns
+  // Up to 4 or 8 rows leave most of a fragment's columns empty.  The scores of
+  // a lane's 8 tokens then move to PK lanes of its 16 (2 or 4 to each), where
+  // exp and the rest of the softmax run without empty lanes, and back as
+  // packed fp16.
+  static constexpr int PK = ROWS < 16 ? 16 / ROWS : 1;
+  static constexpr int kPer = 8 / PK;                     // scores of a lane and fragment in the softmax
   static constexpr int kDB = D * BITS / 8;          // bytes of a token's codes
   static constexpr int kW = kDB / 16;               // dwords of a lane per half tile, keys or values
   static constexpr int kSteps = D / 32;             // matrix instructions per half tile of S^T
   static constexpr int kJ = D / 16;                 // channels of a sixteenth: accumulators of O^T
-  static constexpr int kRows = 16 * R;
+  static constexpr int kRows = ROWS;
   static constexpr int kRegs = R * kJ * 4;          // accumulator registers of a lane
   static constexpr int kRound = 8;                  // accumulators (of 4) per round through LDS
-  static constexpr int kLdsFloats = kAttnWaves * kRound * 4 * 64;
   using KC = KeyCodes<FP16, BITS>;
 
-  struct Tile {
-    uint32_t k[2][kW], v[2][kW];
-    v4f ks[2], vs[2];
-  };
+  // A tile in LDS: the half tiles' keys and values (16 tokens each), 4 x 16 kDB
+  // bytes, then 32 key and 32 value scales.
+  static constexpr int kHalf = 16 * kDB;
+  static constexpr int kTileBytes = 4 * kHalf + 256;
+  static constexpr int kLoads = 4 * kHalf / 1024 + 1;    // loads to a tile
+  // Tiles in flight to a wave: LDS for four workgroups to a CU where a tile is
+  // 4 KB or less.
+  static constexpr int kDepth = kDB == 32 ? 4 : 2;
+  static constexpr int kRingBytes = kDepth * kTileBytes;
+  static constexpr int kJoinBytes = kAttnWaves * kRound * 4 * 64 * 4;
+  static constexpr int kLdsBytes = kAttnWaves * kRingBytes > kJoinBytes ? kAttnWaves * kRingBytes : kJoinBytes;
+
   struct State {
     v4f o[R][kJ];
-    float m[R], l[R], vref;
+    float m[R], l[R];
   };
 
   static __device__ __forceinline__ v4f mma(const v4u& a, const v4u& b, const v4f& c) {
@@ -164,126 +226,241 @@ struct Attn {
       return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, a), __builtin_bit_cast(v8b, b), c, 0, 0,
                                                      0);
   }
+  static __device__ __forceinline__ v4f mma_h(const v4u& a, const v4u& b, const v4f& c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+  }
 
-  // base: the half tiles' first token as a row of [pages][Hkv][page].
-  static __device__ __forceinline__ void load(const AttnArgs& a, const int64_t* base, int lane, Tile& t) {
+  // Where the lane's 16 bytes of a load lie in the 1024 that it moves, keys and
+  // values (kDB = 32: in the 512 of its half tile).  Keys: chunk c of row m is
+  // stored at c ^ key_swizzle(m), values with four chunks to a unit at
+  // i ^ (unit / 4).
+  static __device__ __forceinline__ uint32_t key_swizzle(uint32_t m) {
+    if constexpr (kDB == 32) return (m >> 3) & 1;
+    else if constexpr (kDB == 64) return (m >> 2) & 3;
+    else if constexpr (kDB == 128) return m & 7;
+    else return m & 15;
+  }
+  static __device__ __forceinline__ uint32_t value_swizzle(uint32_t unit) {
+    return kDB == 256 ? (unit >> 2) & 3 : 0;
+  }
+
+  struct Lane {
+    uint32_t k[4], v;           // offsets of the lane's bytes in global memory; k: per load of a half tile (kDB = 256)
+    const uint8_t* scales;      // its scale at row 0
+    uint32_t lk, lv, ls;        // offsets of its keys, values and scales in a tile in LDS
+    int tok;                    // the first token whose probability it computes
+    int lane;
+  };
+  static __device__ __forceinline__ Lane lane_of(const AttnArgs& a, int lane) {
+    Lane l;
     const uint32_t m = lane & 15, g = lane >> 4;
+    constexpr uint32_t kChunks = kDB / 16;              // 16-byte chunks of a row
+    const uint32_t at = kDB == 32 ? lane & 31 : lane;   // position in the load, in chunks
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      load_words<kW>(t.k[h], a.k + base[h] * kDB + (m * kDB + g * (kDB / 4)));
-      t.ks[h] = *reinterpret_cast<const v4f*>(a.ks + base[h] + 4 * g);
+    for (uint32_t i = 0; i < 4; ++i) {
+      const uint32_t row = (at + 64 * i) / kChunks, c = at % kChunks;
+      l.k[i] = row * kDB + ((c ^ key_swizzle(row)) << 4);
     }
+    // (a load of 64 chunks is 16 units of 4: the same pattern in each load)
+    l.v = kDB == 256 ? (at & ~3u) * 16 + (((at & 3) ^ value_swizzle(at >> 2)) << 4) : at * 16;
+    l.scales = reinterpret_cast<const uint8_t*>((lane < 32 ? a.ks : a.vs) + m);
+    l.lk = m * kDB;
+    l.lv = 2 * kHalf + (g * 16 + m) * (kDB / 4);
+    const uint32_t v0 = PK == 1 ? 0 : (m / ROWS) * kPer;   // the lane's first score of its row's eight
+    l.tok = 16 * (v0 >> 2) + 4 * g + (v0 & 3);
+    l.ls = 4 * kHalf + l.tok * 4;
+    l.lane = lane;
+    return l;
+  }
+
+  // base0, base1: the half tiles' first token as a row of [pages][Hkv][page].
+  static __device__ __forceinline__ void load(const AttnArgs& a, const Lane& l, int64_t base0, int64_t base1, uint32_t lds) {
+    if constexpr (kDB == 32) {
+      const int64_t row = l.lane & 32 ? base1 : base0;
+      dma_rows_at(a.k + row * kDB + l.k[0], lds);
+      dma_rows_at(a.v + row * kDB + l.v, lds + 1024);
+    } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      load_words<kW>(t.v[h], a.v + base[h] * kDB + (g * 4 * kDB + m * (kDB / 4)));
-      t.vs[h] = *reinterpret_cast<const v4f*>(a.vs + base[h] + 4 * g);
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < kHalf / 1024; ++i) dma_rows(a.k + (h ? base1 : base0) * kDB, l.k[i], lds + h * kHalf + i * 1024);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < kHalf / 1024; ++i)
+          dma_rows(a.v + (h ? base1 : base0) * kDB + i * 1024, l.v, lds + (2 + h) * kHalf + i * 1024);
+    }
+    dma_word_at(l.scales + 4 * (l.lane & 16 ? base1 : base0), lds + 4 * kHalf);
+  }
+
+  // Half h of a tile in LDS: the lane's keys, values, and scales.
+  static __device__ __forceinline__ void keys(const uint8_t* tile, const Lane& l, int h, uint32_t* w) {
+    const uint32_t m = l.lane & 15, g = l.lane >> 4;
+    if constexpr (kDB == 32) {
+      const uint2 v = *reinterpret_cast<const uint2*>(tile + h * kHalf + l.lk + (((g >> 1) ^ key_swizzle(m)) << 4) +
+                                                      (g & 1) * 8);
+      w[0] = v.x;
+      w[1] = v.y;
+    } else {
+#pragma unroll
+      for (uint32_t i = 0; i < kDB / 64; ++i) {
+        const uint32_t c = (g * (kDB / 64) + i) ^ key_swizzle(m);
+        const v4u v = *reinterpret_cast<const v4u*>(tile + h * kHalf + l.lk + (c << 4));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[4 * i + j] = v[j];
+      }
+    }
+  }
+  static __device__ __forceinline__ void values_of(const uint8_t* tile, const Lane& l, int h, uint32_t* w) {
+    if constexpr (kDB == 32) {
+      const uint2 v = *reinterpret_cast<const uint2*>(tile + h * kHalf + l.lv);
+      w[0] = v.x;
+      w[1] = v.y;
+    } else {
+#pragma unroll
+      for (uint32_t i = 0; i < kDB / 64; ++i) {
+        const uint32_t c = i ^ value_swizzle(l.lane);
+        const v4u v = *reinterpret_cast<const v4u*>(tile + h * kHalf + l.lv + (c << 4));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[4 * i + j] = v[j];
+      }
     }
   }
 
-  // Token t0 .. t0 + 31 of the sequence.  seen: the keys that the lane's rows
-  // see; all: whether every row sees the whole tile.
-  static __device__ __forceinline__ void compute(const Tile& t, const v4u (*qf)[kSteps], const float* c0,
-                                                 float scale_log2, int t0, bool all, int L, const int* seen, int lane,
-                                                 State& st) {
-    const int g = lane >> 4;
-    v4f s[R][2], vs[2];
+  // The scores of a tile in codes.
+  static __device__ __forceinline__ void scores(const uint8_t* tile, const Lane& l, const v4u (*qf)[kSteps],
+                                                const float* c0, const Exponents& e, v4f (*s)[2]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      uint32_t w[kW];
+      keys(tile, l, h, w);
 #pragma unroll
       for (int r = 0; r < R; ++r) s[r][h] = v4f{c0[r], c0[r], c0[r], c0[r]};
 #pragma unroll
       for (int j = 0; j < kSteps; ++j) {
-        const v4u ko = KC::operand(t.k[h] + j * (BITS / 4));
+        const v4u ko = KC::operand(w + j * (BITS / 4), e.key);
 #pragma unroll
         for (int r = 0; r < R; ++r) s[r][h] = mma(ko, qf[r][j], s[r][h]);
       }
-      const v4f f = t.ks[h] * scale_log2;
+    }
+  }
+
+  // The probabilities of tokens t0 .. t0 + 31 of the sequence, times the value
+  // scales, as fp16.  seen: the keys that the lane's rows see; all: whether
+  // every row sees the whole tile.
+  static __device__ __forceinline__ void softmax(const uint8_t* tile, const Lane& l, const v4f (*sc)[2],
+                                                 float scale_log2, int t0, bool all, int L, const int* seen, State& st,
+                                                 v4u* pf) {
+    // score i of the lane: token l.tok + (i & 3) of half tile i / 4
+    float s[R][kPer], f[kPer], vs[kPer];
+    if constexpr (kPer == 2) {
+      const v2f k = *reinterpret_cast<const v2f*>(tile + l.ls), v = *reinterpret_cast<const v2f*>(tile + l.ls + 128);
 #pragma unroll
-      for (int r = 0; r < R; ++r) s[r][h] *= f;
-      vs[h] = t.vs[h];
+      for (int i = 0; i < 2; ++i) {
+        f[i] = k[i] * scale_log2;
+        vs[i] = v[i];
+        s[0][i] = from_below<4, 2>(sc[0][0][i], sc[0][0][2 + i]);
+        s[0][i] = from_below<8, 4>(s[0][i], sc[0][1][i]);
+        s[0][i] = from_below<12, 8>(s[0][i], sc[0][1][2 + i]);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < kPer / 4; ++h) {
+        const v4f k = *reinterpret_cast<const v4f*>(tile + l.ls + 64 * h);
+        const v4f v = *reinterpret_cast<const v4f*>(tile + l.ls + 128 + 64 * h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f[4 * h + i] = k[i] * scale_log2;
+          vs[4 * h + i] = v[i];
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+            s[r][4 * h + i] = kPer == 4 ? from_below<8, 12>(sc[0][0][i], sc[0][1][i]) : sc[r][h][i];
+        }
+      }
     }
     if (!all) {
       // what lies behind a row's last key may be anything, NaN among it
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int i = 0; i < kPer; ++i) {
+        const int tok = t0 + l.tok + 16 * (i >> 2) + (i & 3);
+        vs[i] = tok < L ? vs[i] : 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int tok = t0 + 16 * h + 4 * g + i;
-          vs[h][i] = tok < L ? vs[h][i] : 0.f;
-#pragma unroll
-          for (int r = 0; r < R; ++r) s[r][h][i] = tok < seen[r] ? s[r][h][i] : -__builtin_inff();
-        }
+        for (int r = 0; r < R; ++r) s[r][i] = tok < seen[r] ? s[r][i] * f[i] : -__builtin_inff();
+        f[i] = 1.f;
+      }
     }
-    float c = kLift / st.vref;
-    float p[R][8], pv[R][8], top = 0.f;
+    float sum[R];
+    uint32_t pair[R][kPer / 2];
     auto probabilities = [&] {
-      top = 0.f;
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          p[r][i] = exp2_hw(s[r][i >> 2][i & 3] - st.m[r]);
-          pv[r][i] = p[r][i] * (vs[i >> 2][i & 3] * c);
-          top = fmaxf(top, pv[r][i]);
-        }
-    };
-    probabilities();
-    if (__ballot(top > kLimit || st.m[0] == kUnset) != 0) {
-      // the references move to the largest so far
-      float vm = st.vref;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) vm = fmaxf(vm, vs[i >> 2][i & 3]);
-      vm = row_max(vm);
-      const float fv = st.vref / vm;
-      st.vref = vm;
-      c = kLift / vm;
+      float top = 0.f;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        float sm = st.m[r];
+        float part[kPer / 2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sm = fmaxf(sm, s[r][i >> 2][i & 3]);
-        sm = row_max(sm);
-        const float f = exp2_hw(st.m[r] - sm);
-        st.m[r] = sm;
-        st.l[r] *= f;
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) st.o[r][j] *= f * fv;
+        for (int i = 0; i < kPer / 2; ++i) {
+          const float p0 = exp2_hw(__builtin_fmaf(s[r][2 * i], f[2 * i], -st.m[r]));
+          const float p1 = exp2_hw(__builtin_fmaf(s[r][2 * i + 1], f[2 * i + 1], -st.m[r]));
+          const v2f x = {p0 * vs[2 * i], p1 * vs[2 * i + 1]};
+          top = fmaxf(top, fmaxf(x[0], x[1]));
+          part[i] = p0 + p1;
+          pair[r][i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, v2h));
+        }
+        sum[r] = part[0];
+        if constexpr (kPer == 4) sum[r] = part[0] + part[1];
+        if constexpr (kPer == 8) sum[r] = (part[0] + part[1]) + (part[2] + part[3]);
       }
-      probabilities();
+      return top;
+    };
+    bool over = probabilities() > kTermLimit;
+#pragma unroll
+    for (int r = 0; r < R; ++r) over |= sum[r] > kSumLimit;
+    if (__builtin_expect(__builtin_amdgcn_readfirstlane((int)(__ballot(over) != 0)), 0)) {
+      // the references move to the largest term so far
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float em = -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) em = fmaxf(em, s[r][i] * f[i] + __log2f(fmaxf(vs[i], kTinyScale)));
+        em = fmaxf(st.m[r], row_max<16 / PK>(em) - kLift);
+        const float by = exp2_hw(st.m[r] - em);
+        st.m[r] = em;
+        st.l[r] *= by;
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) st.o[r][j] *= by;
+      }
+      (void)probabilities();
     }
-    v4u pf[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
+      st.l[r] += sum[r];
+      if constexpr (PK == 1) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const v2f x = {pv[r][2 * i], pv[r][2 * i + 1]};
-        pf[r][i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, v2h));
+        for (int i = 0; i < 4; ++i) pf[r][i] = pair[r][i];
+      } else if constexpr (PK == 2) {
+        pf[r] = v4u{pair[r][0], pair[r][1], from_above<8>(pair[r][0]), from_above<8>(pair[r][1])};
+      } else {
+        pf[r] = v4u{pair[r][0], from_above<4>(pair[r][0]), from_above<8>(pair[r][0]), from_above<12>(pair[r][0])};
       }
-      st.l[r] += ((p[r][0] + p[r][1]) + (p[r][2] + p[r][3])) + ((p[r][4] + p[r][5]) + (p[r][6] + p[r][7]));
     }
-    values(t, pf, st);
   }
 
-  // O^T += V^T P^T: accumulator j holds channel j of each sixteenth.
-  static __device__ __forceinline__ void values(const Tile& t, const v4u* pf, State& st) {
-    value_bytes<0>(t, pf, st);
-  }
-
+  // O^T += V^T P^T: accumulator j holds channel j of each sixteenth.  From byte
+  // B of the sixteenths on.
   template <int B>
-  static __device__ __forceinline__ void value_bytes(const Tile& t, const v4u* pf, State& st) {
+  static __device__ __forceinline__ void values(const uint32_t (*w)[kW], const v4u* pf, const Exponents& e, State& st) {
     if constexpr (B < kDB / 16) {
       uint32_t x[4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        x[2 * h] = token_pair<kDB / 16, 0, B>(t.v[h]);
-        x[2 * h + 1] = token_pair<kDB / 16, 2, B>(t.v[h]);
+        x[2 * h] = token_pair<kDB / 16, 0, B>(w[h]);
+        x[2 * h + 1] = token_pair<kDB / 16, 2, B>(w[h]);
       }
       if constexpr (BITS == 4) {
         v4u lo, hi;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          lo[i] = less((x[i] & 0x000F000Fu) | 0x64006400u, 1032.f);
-          hi[i] = less((x[i] & 0x00F000F0u) | 0x54005400u, 72.f);
+          lo[i] = less((x[i] & 0x000F000Fu) | e.lo, 1032.f);
+          hi[i] = less((x[i] & 0x00F000F0u) | e.hi, 72.f);
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -293,15 +470,15 @@ struct Attn {
       } else {
         v4u u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) u[i] = less((x[i] ^ 0x00800080u) | 0x64006400u, 1152.f);
+        for (int i = 0; i < 4; ++i) u[i] = less(x[i] ^ e.lo, 1152.f);
 #pragma unroll
         for (int r = 0; r < R; ++r) st.o[r][B] = mma_h(u, pf[r], st.o[r][B]);
       }
-      value_bytes<B + 1>(t, pf, st);
+      values<B + 1>(w, pf, e, st);
     }
   }
-  static __device__ __forceinline__ v4f mma_h(const v4u& a, const v4u& b, const v4f& c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+  static __device__ __forceinline__ Exponents exponents() {
+    return {held(KC::kExp), held(BITS == 4 ? 0x64006400u : 0x64806480u), held(0x54005400u)};
   }
 };
 
@@ -388,15 +565,22 @@ __device__ __forceinline__ v2f* piece_ml(const AttnArgs& a, uint32_t x, int row)
   return reinterpret_cast<v2f*>(a.part_ml) + (int64_t)x * ROWS + row;
 }
 
-template <bool FP16, int D, int BITS, int R>
-__global__ __launch_bounds__(64 * kAttnWaves, D == 256 || (D == 128 && R == 2) ? 1 : 2) void k_attn(AttnArgs a) {
-  using A = Attn<FP16, D, BITS, R>;
-  __shared__ __align__(16) float lds[A::kLdsFloats];
+template <bool FP16, int D, int BITS, int ROWS>
+__global__ __launch_bounds__(64 * kAttnWaves, D == 256 || ROWS > 16 ? 2 : 4) void k_attn(AttnArgs a) {
+  using A = Attn<FP16, D, BITS, ROWS>;
+  constexpr int R = A::R;
+  __shared__ __align__(16) uint8_t ring[A::kLdsBytes];
+  float* const lds = reinterpret_cast<float*>(ring);
   __shared__ float ldm[kAttnWaves][A::kRows], ldl[kAttnWaves][A::kRows];
   __shared__ uint32_t red[kAttnWaves + 2];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, col = lane & 15;
+  const int own = ROWS < 16 ? col & (ROWS - 1) : col;   // the row whose reference and sum the lane holds
   const int page = a.sh.page;
+  const Exponents e = A::exponents();
+  const typename A::Lane ln = A::lane_of(a, lane);
+  const uint8_t* const mine = ring + wave * A::kRingBytes;
+  const uint32_t mine_at = lds_addr(mine);
 
   const AttnFind f = find_units<64 * kAttnWaves>(a, blockIdx.x, red);
   const uint32_t share = f.share;
@@ -433,10 +617,9 @@ __global__ __launch_bounds__(64 * kAttnWaves, D == 256 || (D == 128 && R == 2) ?
     typename A::State st;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const uint32_t row = row_0 + 16 * r + col;
-      const bool there = row < rows;
-      const uint32_t i = row / (uint32_t)a.sh.G;
-      seen[r] = there ? attn_seen(a.sh, sq, (int)i) : 0;
+      const uint32_t row = row_0 + 16 * r + own, i = row / (uint32_t)a.sh.G;
+      seen[r] = row < rows ? attn_seen(a.sh, sq, (int)i) : 0;
+      const bool there = row < rows && col < ROWS;
       const uint16_t* src = static_cast<const uint16_t*>(a.q) + ((int64_t)sq.row0 + i) * a.q_stride +
                             (int64_t)(h * a.sh.G + (int)(row - i * a.sh.G)) * D + g * (D / 4);
       float sum = 0.f;
@@ -457,47 +640,71 @@ __global__ __launch_bounds__(64 * kAttnWaves, D == 256 || (D == 128 && R == 2) ?
           qf[r][j] = w;
         }
       }
-      c0[r] = -A::KC::kOffset * row_sum(sum);
+      c0[r] = -A::KC::kOffset * row_sum<16>(sum);
       st.m[r] = kUnset;
       st.l[r] = 0.f;
 #pragma unroll
       for (int j = 0; j < A::kJ; ++j) st.o[r][j] = v4f{0.f, 0.f, 0.f, 0.f};
     }
-    st.vref = 1e-30f;
 
+    // The wave's tiles one behind the other, in half tiles of 16 tokens (which
+    // lie in one page).  The pages are in a register, 64 at a time: a page id
+    // costs a lane read, not a load between the tiles.  Behind the sequence's
+    // last page the last one is read again, and nothing of it counts.
     const int32_t* table = a.table + (int64_t)b * a.sh.max_pages;
-    auto where = [&](uint32_t t, int64_t* at) {
-      const uint32_t tok = t * kAttnTile;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        // a half without tokens takes the first half's page: nothing of it counts
-        const uint32_t tk = tok + 16 * x < (uint32_t)sq.L ? tok + 16 * x : tok;
-        const uint32_t n = tk / (uint32_t)page;
-        uint32_t pg = (uint32_t)table[n];
-        if (pg >= (uint32_t)a.pages) pg = 0;   // no page of the cache: any row, and no fault
-        at[x] = ((int64_t)pg * a.sh.Hkv + h) * page + (tk - n * page);
-      }
-    };
     if (t0 < t1) {
-      typename A::Tile x, y;
-      int64_t at[2];
-      where(t0, at);
-      A::load(a, at, lane, x);
-      for (uint32_t t = t0; t < t1; t += 2) {
-        if (t + 1 < t1) {
-          where(t + 1, at);
-          A::load(a, at, lane, y);
+      const uint32_t page_last = ((uint32_t)sq.L - 1) / (uint32_t)page;
+      uint32_t n = t0 * kAttnTile / (uint32_t)page, off = t0 * kAttnTile - n * page;
+      uint32_t ids = 0, ids_from = n - 64;
+      const uint32_t head_rows = (uint32_t)a.sh.Hkv * page, head = (uint32_t)h * page;
+      auto next = [&] {
+        const uint32_t nc = n < page_last ? n : page_last;
+        if (nc - ids_from >= 64) {
+          ids_from = nc;
+          ids = nc + lane <= page_last ? (uint32_t)table[nc + lane] : 0u;
+          if (ids >= (uint32_t)a.pages) ids = 0;   // no page of the cache: any row, and no fault
         }
-        A::compute(x, qf, c0, a.scale_log2, (int)t * kAttnTile, (int)(t + 1) * kAttnTile <= seen_least, sq.L, seen,
-                   lane, st);
-        if (t + 1 < t1) {
-          if (t + 2 < t1) {
-            where(t + 2, at);
-            A::load(a, at, lane, x);
-          }
-          A::compute(y, qf, c0, a.scale_log2, (int)(t + 1) * kAttnTile, (int)(t + 2) * kAttnTile <= seen_least, sq.L,
-                     seen, lane, st);
+        const uint32_t pg = (uint32_t)__builtin_amdgcn_readlane((int)ids, (int)(nc - ids_from));
+        const int64_t at = (int64_t)((uint64_t)pg * head_rows + (head + off));
+        off += 16;
+        if (off == (uint32_t)page) {
+          off = 0;
+          ++n;
         }
+        return at;
+      };
+      uint32_t put = 0, got = 0;      // the ring's places, in bytes
+      auto load = [&] {
+        const int64_t at0 = next(), at1 = next();
+        A::load(a, ln, at0, at1, mine_at + put);
+        put = put == A::kRingBytes - A::kTileBytes ? 0 : put + A::kTileBytes;
+      };
+      wait_loads<0>();                // only the tiles' loads are counted from here on
+#pragma unroll
+      for (int d = 0; d < A::kDepth; ++d)
+        if (t0 + d < t1) load();
+      for (uint32_t t = t0; t < t1; ++t) {
+        // the loads of the tiles behind this one may be outstanding
+        const uint32_t behind = t1 - 1 - t;
+        if (A::kDepth > 3 && behind >= 3) wait_loads<(A::kDepth > 3 ? 3 * A::kLoads : 0)>();
+        else if (A::kDepth > 2 && behind >= 2) wait_loads<(A::kDepth > 2 ? 2 * A::kLoads : 0)>();
+        else if (behind >= 1) wait_loads<A::kLoads>();
+        else wait_loads<0>();
+        const uint8_t* tile = mine + got;
+        v4f s[R][2];
+        v4u pf[R];
+        A::scores(tile, ln, qf, c0, e, s);
+        A::softmax(tile, ln, s, a.scale_log2, (int)t * kAttnTile, (int)(t + 1) * kAttnTile <= seen_least, sq.L, seen,
+                   st, pf);
+        uint32_t w[2][A::kW];
+        A::values_of(tile, ln, 0, w[0]);
+        A::values_of(tile, ln, 1, w[1]);
+        if (t + A::kDepth < t1) {
+          wait_lds_reads();
+          load();
+        }
+        A::template values<0>(w, pf, e, st);
+        got = got == A::kRingBytes - A::kTileBytes ? 0 : got + A::kTileBytes;
       }
     }
 
@@ -507,22 +714,22 @@ __global__ __launch_bounds__(64 * kAttnWaves, D == 256 || (D == 128 && R == 2) ?
     float fw[R], M[R], Ls[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      st.l[r] = row_sum(st.l[r]);
-      if (g == 0) {
+      st.l[r] = row_sum<16 / A::PK>(st.l[r]);
+      if (g == 0 && col < ROWS) {
         ldm[wave][16 * r + col] = st.m[r];
         ldl[wave][16 * r + col] = st.l[r];
       }
     }
-    __syncthreads();
+    __syncthreads();   // and every wave is through with its ring
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      M[r] = ldm[0][16 * r + col];
+      M[r] = ldm[0][16 * r + own];
 #pragma unroll
-      for (int w = 1; w < kAttnWaves; ++w) M[r] = fmaxf(M[r], ldm[w][16 * r + col]);
+      for (int w = 1; w < kAttnWaves; ++w) M[r] = fmaxf(M[r], ldm[w][16 * r + own]);
       Ls[r] = 0.f;
 #pragma unroll
-      for (int w = 0; w < kAttnWaves; ++w) Ls[r] += ldl[w][16 * r + col] * exp2_hw(ldm[w][16 * r + col] - M[r]);
-      fw[r] = exp2_hw(st.m[r] - M[r]) * (st.vref * (1.f / kLift));
+      for (int w = 0; w < kAttnWaves; ++w) Ls[r] += ldl[w][16 * r + own] * exp2_hw(ldm[w][16 * r + own] - M[r]);
+      fw[r] = exp2_hw(st.m[r] - M[r]);
       if (whole) fw[r] = Ls[r] > 0.f ? fw[r] / Ls[r] : 0.f;
     }
     constexpr int kAcc = R * A::kJ;
@@ -550,7 +757,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, D == 256 || (D == 128 && R == 2) ?
         }
         const int r = (n0 + nn) / A::kJ, j = (n0 + nn) % A::kJ;
         const uint32_t row = row_0 + 16 * r + col;
-        if (row < rows) {
+        if (row < rows && col < ROWS) {
           if (whole) {
             store_pair<FP16, D>(a, out_row(a, sq, h, row), g, j, sum[0], sum[1]);
           } else {
@@ -564,9 +771,9 @@ __global__ __launch_bounds__(64 * kAttnWaves, D == 256 || (D == 128 && R == 2) ?
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const uint32_t row = row_0 + 16 * r + col;
-        if (row < rows) {
+        if (row < rows && col < ROWS) {
           if (!whole) *piece_ml<A::kRows>(a, piece, 16 * r + col) = v2f{M[r], Ls[r]};
-          else if (a.lse) a.lse[out_row(a, sq, h, row)] = Ls[r] > 0.f ? M[r] * kLn2 + __logf(Ls[r]) : -__builtin_inff();
+          else if (a.lse) a.lse[out_row(a, sq, h, row)] = log_sum(M[r], Ls[r]);
         }
       }
     }
@@ -578,9 +785,9 @@ __global__ __launch_bounds__(64 * kAttnWaves, D == 256 || (D == 128 && R == 2) ?
 // Segments that more than one workgroup holds: workgroup w joins the one that
 // w is the first to hold and w + 1 goes on with, if there is one.  Each wave
 // takes accumulators of its own and all pieces in order.
-template <bool FP16, int D, int R>
+template <bool FP16, int D, int ROWS>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-  constexpr int kJ = D / 16, kAcc = R * kJ, kRows = 16 * R;
+  constexpr int kJ = D / 16, kAcc = (ROWS > 16 ? ROWS / 16 : 1) * kJ, kRows = ROWS;
   __shared__ uint32_t red[6];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, col = lane & 15;
@@ -599,7 +806,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   for (int n = wave; n < kAcc; n += 4) {
     const int r = n / kJ, j = n % kJ;
     const uint32_t row = row_0 + 16 * r + col;
-    if (row >= rows) continue;
+    if (row >= rows || col >= ROWS) continue;
     float M = kUnset, Ls = 0.f;
     v4f o = {0.f, 0.f, 0.f, 0.f};
     for (uint32_t w = blockIdx.x; w <= wl; ++w) {
@@ -616,38 +823,48 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     uint16_t* out = static_cast<uint16_t*>(a.out) + orow * D;
 #pragma unroll
     for (int i = 0; i < 4; ++i) out[(4 * g + i) * kJ + j] = (uint16_t)to16<FP16>(o[i] * inv, 0.f);
-    if (a.lse && j == 0 && g == 0) a.lse[orow] = Ls > 0.f ? M * kLn2 + __logf(Ls) : -__builtin_inff();
+    if (a.lse && j == 0 && g == 0) a.lse[orow] = log_sum(M, Ls);
   }
 }
 
-template <bool FP16, int D, int BITS, int R>
+template <bool FP16, int D, int BITS, int ROWS>
 hipError_t attn_go(const AttnArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((k_attn<FP16, D, BITS, R>), dim3((unsigned)a.workgroups), dim3(64 * kAttnWaves), 0, st, a);
+  hipLaunchKernelGGL((k_attn<FP16, D, BITS, ROWS>), dim3((unsigned)a.workgroups), dim3(64 * kAttnWaves), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.workgroups == 1) return e;
-  hipLaunchKernelGGL((k_attn_join<FP16, D, R>), dim3((unsigned)a.workgroups - 1), dim3(256), 0, st, a);
+  hipLaunchKernelGGL((k_attn_join<FP16, D, ROWS>), dim3((unsigned)a.workgroups - 1), dim3(256), 0, st, a);
   return hipGetLastError();
+}
+
+template <bool FP16, int D, int BITS>
+hipError_t attn_rows(const AttnArgs& a, hipStream_t st) {
+  switch (a.sh.rows) {
+    case 4: return attn_go<FP16, D, BITS, 4>(a, st);
+    case 8: return attn_go<FP16, D, BITS, 8>(a, st);
+    case 16: return attn_go<FP16, D, BITS, 16>(a, st);
+    default:
+      if constexpr (D < 256) return attn_go<FP16, D, BITS, 32>(a, st);
+      return hipErrorInvalidValue;
+  }
 }
 
 template <bool FP16, int D>
 hipError_t attn_pick(const AttnArgs& a, int bits, hipStream_t st) {
-  if constexpr (D < 256) {
-    if (a.sh.rows == 32) return bits == 4 ? attn_go<FP16, D, 4, 2>(a, st) : attn_go<FP16, D, 8, 2>(a, st);
-  }
-  return bits == 4 ? attn_go<FP16, D, 4, 1>(a, st) : attn_go<FP16, D, 8, 1>(a, st);
+  return bits == 4 ? attn_rows<FP16, D, 4>(a, st) : attn_rows<FP16, D, 8>(a, st);
 }
 
 }  // namespace
 
 // Rows to a row tile, workgroups and workspace of a call.
 int64_t attn_workspace(AttnArgs* a, int64_t D, void* ws) {
-  a->sh.rows = (int64_t)a->sh.max_q * a->sh.G <= 16 || D == 256 ? 16 : 32;
-  a->workgroups = 1024;
-  const int64_t pieces = 2 * (int64_t)a->workgroups;
-  const int64_t o = pieces * a->sh.rows * D * 4;
+  const int64_t rows = (int64_t)a->sh.max_q * a->sh.G;
+  a->sh.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 || D == 256 ? 16 : 32;
+  a->workgroups = 512;
+  const int64_t pieces = 2 * (int64_t)a->workgroups, kept = a->sh.rows < 16 ? 16 : a->sh.rows;
+  const int64_t o = pieces * kept * D * 4;
   a->part = static_cast<float*>(ws);
   a->part_ml = ws ? reinterpret_cast<float*>(static_cast<char*>(ws) + o) : nullptr;
-  return o + pieces * a->sh.rows * 8;
+  return o + pieces * kept * 8;
 }
 
 hipError_t launch_attn(const AttnArgs& a, bool fp16, int bits, int D, hipStream_t st) {
