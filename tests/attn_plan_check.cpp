@@ -1,7 +1,8 @@
 // CPU check of csrc/attn_plan.h: the walk of the attention kernel's workgroups
 // over units, and that of the joining kernel over pieces, on random sequences.
 // Every tile of every segment is taken once, a segment's pieces are the ones
-// that the joining kernel reads, in places that nothing else writes.
+// that the joining kernel reads, in places that nothing else writes, and a
+// workgroup begins one shared segment at most.
 #include <cstdio>
 #include <cstdlib>
 #include <map>
@@ -67,32 +68,34 @@ int main() {
     CHECK((uint64_t)share * workgroups >= total);
     std::map<Segment, std::vector<int>> taken;               // times each tile is taken
     std::map<Segment, std::vector<uint32_t>> pieces;         // places, in order of workgroups
-    std::set<Segment> whole;
+    std::map<Segment, std::pair<uint32_t, uint32_t>> split;  // the workgroup that began it, followers
     std::set<uint32_t> used;
     for (uint32_t w = 0; w < workgroups; ++w) {
       const uint32_t lo = w * share, hi = lo + share < total ? lo + share : total;
-      if (lo >= total) continue;
-      int b = 0;
-      while (lo >= base[b + 1]) ++b;
+      int splits = 0, b = 0;
+      while (lo < hi && lo >= base[b + 1]) ++b;
       for (uint32_t u = lo; u < hi;) {
         if (u >= base[b + 1]) {
           ++b;
           continue;
         }
         const AttnSeg g = attn_segment(a, seq[b], u - base[b], hi - base[b]);
-        CHECK(g.h >= 0 && g.h < a.Hkv && g.row_0 < g.rows && g.first < g.last && g.last <= g.tiles);
+        CHECK(g.units > 0 && u + g.units <= hi);
+        u += g.units;
+        CHECK(g.h >= 0 && g.h < a.Hkv && g.row_0 < g.rows && g.first <= g.last && g.last <= g.tiles);
+        if (g.first == g.last) continue;
         const Segment s(b, g.h, g.row_0);
         auto& t = taken[s];
         t.resize(g.tiles);
         for (uint32_t i = g.first; i < g.last; ++i) ++t[i];
-        if (g.first == 0 && g.last == g.tiles) {
-          whole.insert(s);
-        } else {
-          const uint32_t x = attn_place(w, u - g.first, share);
-          CHECK(x < 2 * workgroups && used.insert(x).second);
-          pieces[s].push_back(x);
+        if (g.first == 0 && g.last == g.tiles) continue;
+        const uint32_t x = attn_place(w, g.first == 0);
+        CHECK(x < 2 * workgroups && used.insert(x).second);
+        pieces[s].push_back(x);
+        if (g.first == 0) {
+          split[s] = {w, attn_followers(g.tiles, g.last, share)};
+          CHECK(++splits == 1);          // one record to a workgroup
         }
-        u += g.last - g.first;
       }
     }
     uint32_t segments = 0;
@@ -100,23 +103,13 @@ int main() {
     CHECK(taken.size() == segments);
     for (auto& t : taken)
       for (int n : t.second) CHECK(n == 1);
-    for (uint32_t w = 0; w + 1 < workgroups; ++w) {
-      const uint32_t border = (w + 1) * share;
-      if (border >= total) continue;
-      int b = 0;
-      while (border >= base[b + 1]) ++b;
-      const AttnSeg g = attn_segment(a, seq[b], border - base[b], border - base[b] + 1);
-      const uint32_t s0 = border - g.first;
-      if (s0 == border || s0 < w * share) continue;
-      const Segment s(b, g.h, g.row_0);
-      const uint32_t wl = (s0 + g.tiles - 1) / share;
-      CHECK(wl < workgroups && !whole.count(s));
+    CHECK(split.size() == pieces.size());
+    for (auto& s : split) {
+      CHECK(s.second.second > 0 && s.second.first + s.second.second < workgroups);
       std::vector<uint32_t> reads;
-      for (uint32_t v = w; v <= wl; ++v) reads.push_back(attn_place(v, s0, share));
-      CHECK(reads == pieces[s]);
-      pieces.erase(s);
+      for (uint32_t v = 0; v <= s.second.second; ++v) reads.push_back(attn_place(s.second.first + v, v == 0));
+      CHECK(reads == pieces[s.first]);
     }
-    CHECK(pieces.empty());
   }
   std::printf("ok\n");
   return 0;

@@ -482,10 +482,11 @@ struct Attn {
   }
 };
 
-// Query row `row` of a sequence and key head h, as a row of [T][Hq].
-__device__ __forceinline__ int64_t out_row(const AttnArgs& a, const AttnSeq& s, int h, uint32_t row) {
+// Query row `row` of key head h of a sequence whose first token is row0, as a
+// row of [T][Hq].
+__device__ __forceinline__ int64_t out_row(const AttnArgs& a, int row0, int h, uint32_t row) {
   const uint32_t i = row / (uint32_t)a.sh.G;
-  return ((int64_t)s.row0 + i) * (a.sh.Hkv * a.sh.G) + h * a.sh.G + (row - i * a.sh.G);
+  return ((int64_t)row0 + i) * (a.sh.Hkv * a.sh.G) + h * a.sh.G + (row - i * a.sh.G);
 }
 
 __device__ __forceinline__ AttnSeq get_seq(const AttnArgs& a, int b) {
@@ -493,20 +494,26 @@ __device__ __forceinline__ AttnSeq get_seq(const AttnArgs& a, int b) {
   return attn_seq(a.sh, b * a.sh.max_q, (b + 1) * a.sh.max_q, a.kv_lens[b]);
 }
 
-// The sequence that holds a workgroup's first unit (workgroup x of
-// a.workgroups, with shares as attn_share gives them), its own first unit, and
-// the units of all sequences, found by a workgroup of NT threads: each counts
-// those of some neighbouring sequences, and a scan says where they begin.  b
-// and base are set if the workgroup has units.
+// The sequence that holds a workgroup's first unit, its own first unit, the
+// units of all sequences and the workgroup's share of them, found by the
+// workgroup: each thread counts those of some neighbouring sequences, and a
+// scan says where they begin.  b, base and sq are set if the workgroup has
+// units.  red: a word per wave, then kAttnFound.
 struct AttnFind {
   uint32_t total, share, base;
   int b;
+  AttnSeq sq;
 };
-template <int NT>
-__device__ __forceinline__ AttnFind find_units(const AttnArgs& a, uint32_t x, uint32_t* red) {
-  const int tid = threadIdx.x, per = (a.sh.B + NT - 1) / NT, b0 = tid * per;
+constexpr int kAttnFound = 5;
+__device__ __forceinline__ AttnFind find_units(const AttnArgs& a, uint32_t workgroup, uint32_t* red) {
+  constexpr int kThreads = 64 * kAttnWaves;
+  const int tid = threadIdx.x, per = (a.sh.B + kThreads - 1) / kThreads, b0 = tid * per;
+  AttnSeq sq = {0, 0, 0};
   uint32_t sum = 0;
-  for (int b = b0; b < b0 + per && b < a.sh.B; ++b) sum += attn_units(a.sh, get_seq(a, b));
+  for (int b = b0; b < b0 + per && b < a.sh.B; ++b) {
+    sq = get_seq(a, b);
+    sum += attn_units(a.sh, sq);
+  }
   uint32_t in = sum;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -515,25 +522,33 @@ __device__ __forceinline__ AttnFind find_units(const AttnArgs& a, uint32_t x, ui
   }
   if ((tid & 63) == 63) red[tid >> 6] = in;
   __syncthreads();
-  AttnFind f = {0, 0, 0, 0};
+  AttnFind f = {};
 #pragma unroll
-  for (int w = 0; w < NT / 64; ++w) {
+  for (int w = 0; w < kAttnWaves; ++w) {
     if (w < (tid >> 6)) in += red[w];
     f.total += red[w];
   }
   f.share = attn_share(f.total, a.workgroups);
-  const uint32_t want = x * f.share;
+  const uint32_t want = workgroup * f.share;
   if (want >= f.total) return f;
+  uint32_t* const found = red + kAttnWaves;
   if (in - sum <= want && want < in) {   // one thread
     uint32_t base = in - sum;
     int b = b0;
-    for (uint32_t u; want >= base + (u = attn_units(a.sh, get_seq(a, b))); ++b) base += u;
-    red[NT / 64] = base;
-    red[NT / 64 + 1] = (uint32_t)b;
+    if (per > 1)
+      for (uint32_t u; sq = get_seq(a, b), want >= base + (u = attn_units(a.sh, sq)); ++b) base += u;
+    found[0] = base;
+    found[1] = (uint32_t)b;
+    found[2] = (uint32_t)sq.row0;
+    found[3] = (uint32_t)sq.n;
+    found[4] = (uint32_t)sq.L;
   }
   __syncthreads();
-  f.base = __builtin_amdgcn_readfirstlane(red[NT / 64]);
-  f.b = __builtin_amdgcn_readfirstlane((int)red[NT / 64 + 1]);
+  f.base = __builtin_amdgcn_readfirstlane(found[0]);
+  f.b = __builtin_amdgcn_readfirstlane((int)found[1]);
+  f.sq.row0 = __builtin_amdgcn_readfirstlane((int)found[2]);
+  f.sq.n = __builtin_amdgcn_readfirstlane((int)found[3]);
+  f.sq.L = __builtin_amdgcn_readfirstlane((int)found[4]);
   return f;
 }
 
@@ -560,19 +575,25 @@ template <int N, int ROWS>
 __device__ __forceinline__ v4f* piece_o(const AttnArgs& a, uint32_t x, int n, int lane) {
   return reinterpret_cast<v4f*>(a.part) + ((int64_t)x * N + n) * 64 + lane;
 }
+// A segment that a workgroup begins and others go on with, for the kernel that
+// joins the pieces: a record per workgroup, followers 0 where there is none.
+struct AttnSplit {
+  uint32_t followers, row_0, rows;
+  int row0, h;
+};
 template <int ROWS>
 __device__ __forceinline__ v2f* piece_ml(const AttnArgs& a, uint32_t x, int row) {
   return reinterpret_cast<v2f*>(a.part_ml) + (int64_t)x * ROWS + row;
 }
 
 template <bool FP16, int D, int BITS, int ROWS>
-__global__ __launch_bounds__(64 * kAttnWaves, D == 256 || ROWS > 16 ? 2 : 4) void k_attn(AttnArgs a) {
+__global__ __launch_bounds__(64 * kAttnWaves, 2) void k_attn(AttnArgs a) {
   using A = Attn<FP16, D, BITS, ROWS>;
   constexpr int R = A::R;
   __shared__ __align__(16) uint8_t ring[A::kLdsBytes];
   float* const lds = reinterpret_cast<float*>(ring);
   __shared__ float ldm[kAttnWaves][A::kRows], ldl[kAttnWaves][A::kRows];
-  __shared__ uint32_t red[kAttnWaves + 2];
+  __shared__ uint32_t red[kAttnWaves + kAttnFound];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, col = lane & 15;
   const int own = ROWS < 16 ? col & (ROWS - 1) : col;   // the row whose reference and sum the lane holds
@@ -582,22 +603,23 @@ __global__ __launch_bounds__(64 * kAttnWaves, D == 256 || ROWS > 16 ? 2 : 4) voi
   const uint8_t* const mine = ring + wave * A::kRingBytes;
   const uint32_t mine_at = lds_addr(mine);
 
-  const AttnFind f = find_units<64 * kAttnWaves>(a, blockIdx.x, red);
-  const uint32_t share = f.share;
-  const uint32_t lo = blockIdx.x * share, hi = lo + share < f.total ? lo + share : f.total;
-  if (lo >= f.total) return;
+  const AttnFind f = find_units(a, blockIdx.x, red);
+  const uint32_t lo = blockIdx.x * f.share, hi = lo + f.share < f.total ? lo + f.share : f.total;
+  AttnSplit split = {};
 
   int b = f.b;
   uint32_t base = f.base;
+  AttnSeq sq = f.sq;
   for (uint32_t u = lo; u < hi;) {
-    const AttnSeq sq = get_seq(a, b);
     const uint32_t units = attn_units(a.sh, sq);
     if (u >= base + units) {
       base += units;
-      ++b;
+      sq = get_seq(a, ++b);
       continue;
     }
     const AttnSeg sg = attn_segment(a.sh, sq, u - base, hi - base);
+    u += sg.units;
+    if (sg.first == sg.last) continue;
     const uint32_t tiles = sg.tiles, first = sg.first, last = sg.last, row_0 = sg.row_0, rows = sg.rows;
     const int h = sg.h;
     const uint32_t row_last = row_0 + A::kRows < rows ? row_0 + A::kRows - 1 : rows - 1;
@@ -610,35 +632,76 @@ __global__ __launch_bounds__(64 * kAttnWaves, D == 256 || ROWS > 16 ? 2 : 4) voi
     const uint32_t per = (count + kAttnWaves - 1) / kAttnWaves;
     const uint32_t t0 = first + wave * per, t1 = t0 + per < end ? t0 + per : end;
 
+    // The wave's tiles one behind the other, in half tiles of 16 tokens (which
+    // lie in one page).  The pages are in a register, 64 at a time: a page id
+    // costs a lane read, not a load between the tiles.  Behind the sequence's
+    // last page the last one is read again, and nothing of it counts.
+    const int32_t* table = a.table + (int64_t)b * a.sh.max_pages;
+    const uint32_t page_last = ((uint32_t)sq.L - 1) / (uint32_t)page;
+    uint32_t n = t0 * kAttnTile / (uint32_t)page, off = t0 * kAttnTile - n * page;
+    uint32_t ids = 0, ids_from = n;
+    auto fetch_ids = [&] {
+      ids = ids_from + lane <= page_last ? (uint32_t)table[ids_from + lane] : 0u;
+    };
+    if (t0 < t1) fetch_ids();
     // this lane's rows
     v4u qf[R][A::kSteps];
-    float c0[R];
     int seen[R];
-    typename A::State st;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const uint32_t row = row_0 + 16 * r + own, i = row / (uint32_t)a.sh.G;
       seen[r] = row < rows ? attn_seen(a.sh, sq, (int)i) : 0;
-      const bool there = row < rows && col < ROWS;
       const uint16_t* src = static_cast<const uint16_t*>(a.q) + ((int64_t)sq.row0 + i) * a.q_stride +
                             (int64_t)(h * a.sh.G + (int)(row - i * a.sh.G)) * D + g * (D / 4);
+#pragma unroll
+      for (int j = 0; j < A::kSteps; ++j) {
+        qf[r][j] = v4u{0u, 0u, 0u, 0u};
+        if (row < rows && col < ROWS && t0 < t1) qf[r][j] = *reinterpret_cast<const v4u*>(src + 8 * j);
+      }
+    }
+    wait_loads<0>();                  // only the tiles' loads are counted from here on
+    const uint32_t head_rows = (uint32_t)a.sh.Hkv * page, head = (uint32_t)h * page;
+    auto next = [&] {
+      const uint32_t nc = n < page_last ? n : page_last;
+      if (nc - ids_from >= 64) {
+        ids_from = nc;
+        fetch_ids();
+      }
+      uint32_t pg = (uint32_t)__builtin_amdgcn_readlane((int)ids, (int)(nc - ids_from));
+      if (pg >= (uint32_t)a.pages) pg = 0;   // no page of the cache: any row, and no fault
+      const int64_t at = (int64_t)((uint64_t)pg * head_rows + (head + off));
+      off += 16;
+      if (off == (uint32_t)page) {
+        off = 0;
+        ++n;
+      }
+      return at;
+    };
+    uint32_t put = 0, got = 0;        // the ring's places, in bytes
+    auto load = [&] {
+      const int64_t at0 = next(), at1 = next();
+      A::load(a, ln, at0, at1, mine_at + put);
+      put = put == A::kRingBytes - A::kTileBytes ? 0 : put + A::kTileBytes;
+    };
+#pragma unroll
+    for (int d = 0; d < A::kDepth; ++d)
+      if (t0 + d < t1) load();
+
+    typename A::State st;
+    float c0[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < A::kSteps; ++j) {
-        v4u w = {0u, 0u, 0u, 0u};
-        if (there) w = *reinterpret_cast<const v4u*>(src + 8 * j);
+        const v4u w = qf[r][j];
         float x[8];
         unpack8<FP16>(make_uint4(w[0], w[1], w[2], w[3]), x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum += x[e];
-        if constexpr (BITS == 4) {   // 0 4 1 5 2 6 3 7
-          qf[r][j][0] = __builtin_amdgcn_perm(w[2], w[0], 0x05040100u);
-          qf[r][j][1] = __builtin_amdgcn_perm(w[2], w[0], 0x07060302u);
-          qf[r][j][2] = __builtin_amdgcn_perm(w[3], w[1], 0x05040100u);
-          qf[r][j][3] = __builtin_amdgcn_perm(w[3], w[1], 0x07060302u);
-        } else {
-          qf[r][j] = w;
-        }
+        for (int i = 0; i < 8; ++i) sum += x[i];
+        if constexpr (BITS == 4)       // 0 4 1 5 2 6 3 7
+          qf[r][j] = v4u{__builtin_amdgcn_perm(w[2], w[0], 0x05040100u), __builtin_amdgcn_perm(w[2], w[0], 0x07060302u),
+                         __builtin_amdgcn_perm(w[3], w[1], 0x05040100u), __builtin_amdgcn_perm(w[3], w[1], 0x07060302u)};
       }
       c0[r] = -A::KC::kOffset * row_sum<16>(sum);
       st.m[r] = kUnset;
@@ -646,71 +709,34 @@ __global__ __launch_bounds__(64 * kAttnWaves, D == 256 || ROWS > 16 ? 2 : 4) voi
 #pragma unroll
       for (int j = 0; j < A::kJ; ++j) st.o[r][j] = v4f{0.f, 0.f, 0.f, 0.f};
     }
-
-    // The wave's tiles one behind the other, in half tiles of 16 tokens (which
-    // lie in one page).  The pages are in a register, 64 at a time: a page id
-    // costs a lane read, not a load between the tiles.  Behind the sequence's
-    // last page the last one is read again, and nothing of it counts.
-    const int32_t* table = a.table + (int64_t)b * a.sh.max_pages;
-    if (t0 < t1) {
-      const uint32_t page_last = ((uint32_t)sq.L - 1) / (uint32_t)page;
-      uint32_t n = t0 * kAttnTile / (uint32_t)page, off = t0 * kAttnTile - n * page;
-      uint32_t ids = 0, ids_from = n - 64;
-      const uint32_t head_rows = (uint32_t)a.sh.Hkv * page, head = (uint32_t)h * page;
-      auto next = [&] {
-        const uint32_t nc = n < page_last ? n : page_last;
-        if (nc - ids_from >= 64) {
-          ids_from = nc;
-          ids = nc + lane <= page_last ? (uint32_t)table[nc + lane] : 0u;
-          if (ids >= (uint32_t)a.pages) ids = 0;   // no page of the cache: any row, and no fault
-        }
-        const uint32_t pg = (uint32_t)__builtin_amdgcn_readlane((int)ids, (int)(nc - ids_from));
-        const int64_t at = (int64_t)((uint64_t)pg * head_rows + (head + off));
-        off += 16;
-        if (off == (uint32_t)page) {
-          off = 0;
-          ++n;
-        }
-        return at;
-      };
-      uint32_t put = 0, got = 0;      // the ring's places, in bytes
-      auto load = [&] {
-        const int64_t at0 = next(), at1 = next();
-        A::load(a, ln, at0, at1, mine_at + put);
-        put = put == A::kRingBytes - A::kTileBytes ? 0 : put + A::kTileBytes;
-      };
-      wait_loads<0>();                // only the tiles' loads are counted from here on
-#pragma unroll
-      for (int d = 0; d < A::kDepth; ++d)
-        if (t0 + d < t1) load();
-      for (uint32_t t = t0; t < t1; ++t) {
-        // the loads of the tiles behind this one may be outstanding
-        const uint32_t behind = t1 - 1 - t;
-        if (A::kDepth > 3 && behind >= 3) wait_loads<(A::kDepth > 3 ? 3 * A::kLoads : 0)>();
-        else if (A::kDepth > 2 && behind >= 2) wait_loads<(A::kDepth > 2 ? 2 * A::kLoads : 0)>();
-        else if (behind >= 1) wait_loads<A::kLoads>();
-        else wait_loads<0>();
-        const uint8_t* tile = mine + got;
-        v4f s[R][2];
-        v4u pf[R];
-        A::scores(tile, ln, qf, c0, e, s);
-        A::softmax(tile, ln, s, a.scale_log2, (int)t * kAttnTile, (int)(t + 1) * kAttnTile <= seen_least, sq.L, seen,
-                   st, pf);
-        uint32_t w[2][A::kW];
-        A::values_of(tile, ln, 0, w[0]);
-        A::values_of(tile, ln, 1, w[1]);
-        if (t + A::kDepth < t1) {
-          wait_lds_reads();
-          load();
-        }
-        A::template values<0>(w, pf, e, st);
-        got = got == A::kRingBytes - A::kTileBytes ? 0 : got + A::kTileBytes;
+    for (uint32_t t = t0; t < t1; ++t) {
+      // the loads of the tiles behind this one may be outstanding
+      const uint32_t behind = t1 - 1 - t;
+      if (A::kDepth > 3 && behind >= 3) wait_loads<(A::kDepth > 3 ? 3 * A::kLoads : 0)>();
+      else if (A::kDepth > 2 && behind >= 2) wait_loads<(A::kDepth > 2 ? 2 * A::kLoads : 0)>();
+      else if (behind >= 1) wait_loads<A::kLoads>();
+      else wait_loads<0>();
+      const uint8_t* tile = mine + got;
+      v4f s[R][2];
+      v4u pf[R];
+      A::scores(tile, ln, qf, c0, e, s);
+      A::softmax(tile, ln, s, a.scale_log2, (int)t * kAttnTile, (int)(t + 1) * kAttnTile <= seen_least, sq.L, seen,
+                 st, pf);
+      uint32_t w[2][A::kW];
+      A::values_of(tile, ln, 0, w[0]);
+      A::values_of(tile, ln, 1, w[1]);
+      if (t + A::kDepth < t1) {
+        wait_lds_reads();
+        load();
       }
+      A::template values<0>(w, pf, e, st);
+      got = got == A::kRingBytes - A::kTileBytes ? 0 : got + A::kTileBytes;
     }
 
     // the waves join: common references, then the sums through LDS
     const bool whole = first == 0 && last == tiles;
-    const uint32_t piece = attn_place(blockIdx.x, u - first, share);
+    const uint32_t piece = attn_place(blockIdx.x, first == 0);
+    if (first == 0 && !whole) split = {attn_followers(tiles, last, f.share), row_0, rows, sq.row0, h};
     float fw[R], M[R], Ls[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -759,7 +785,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, D == 256 || ROWS > 16 ? 2 : 4) voi
         const uint32_t row = row_0 + 16 * r + col;
         if (row < rows && col < ROWS) {
           if (whole) {
-            store_pair<FP16, D>(a, out_row(a, sq, h, row), g, j, sum[0], sum[1]);
+            store_pair<FP16, D>(a, out_row(a, sq.row0, h, row), g, j, sum[0], sum[1]);
           } else {
             *piece_o<kAcc, A::kRows>(a, piece, n0 + nn, lane) = sum[0];
             *piece_o<kAcc, A::kRows>(a, piece, n0 + nn + 1, lane) = sum[1];
@@ -773,53 +799,64 @@ __global__ __launch_bounds__(64 * kAttnWaves, D == 256 || ROWS > 16 ? 2 : 4) voi
         const uint32_t row = row_0 + 16 * r + col;
         if (row < rows && col < ROWS) {
           if (!whole) *piece_ml<A::kRows>(a, piece, 16 * r + col) = v2f{M[r], Ls[r]};
-          else if (a.lse) a.lse[out_row(a, sq, h, row)] = log_sum(M[r], Ls[r]);
+          else if (a.lse) a.lse[out_row(a, sq.row0, h, row)] = log_sum(M[r], Ls[r]);
         }
       }
     }
     __syncthreads();   // LDS is free for the next segment
-    u += last - first;
   }
+  if (threadIdx.x == 0) static_cast<AttnSplit*>(a.splits)[blockIdx.x] = split;
 }
 
-// Segments that more than one workgroup holds: workgroup w joins the one that
-// w is the first to hold and w + 1 goes on with, if there is one.  Each wave
-// takes accumulators of its own and all pieces in order.
-template <bool FP16, int D, int ROWS>
-__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-  constexpr int kJ = D / 16, kAcc = (ROWS > 16 ? ROWS / 16 : 1) * kJ, kRows = ROWS;
-  __shared__ uint32_t red[6];
+// The segments that more than one workgroup holds: workgroup w joins the one
+// that workgroup w began, if there is one.  SPREAD: a workgroup to an
+// accumulator, whose waves take turns at the pieces and join in LDS; otherwise
+// a wave to every fourth accumulator, with all pieces in order.
+template <bool FP16, int D, int ROWS, bool SPREAD>
+__global__ __launch_bounds__(64 * kAttnWaves) void k_attn_join(AttnArgs a) {
+  constexpr int kJ = D / 16, kAcc = (ROWS > 16 ? ROWS / 16 : 1) * kJ;
+  const AttnSplit sp = static_cast<const AttnSplit*>(a.splits)[blockIdx.x];
+  if (sp.followers == 0) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, col = lane & 15;
-  const AttnFind f = find_units<256>(a, blockIdx.x + 1, red);
-  const uint32_t share = f.share;
-  const uint32_t border = (blockIdx.x + 1) * share;     // the first unit of the next workgroup
-  if (border >= f.total) return;
-  const uint32_t base = f.base;
-  const AttnSeq sq = get_seq(a, f.b);
-  const AttnSeg sg = attn_segment(a.sh, sq, border - base, border - base + 1);
-  const uint32_t s0 = border - sg.first;               // the segment's first unit
-  if (s0 == border || s0 < blockIdx.x * share) return;  // begins there, or with an earlier workgroup
-  const uint32_t wl = (s0 + sg.tiles - 1) / share;      // the last workgroup that holds some of it
-  const uint32_t row_0 = sg.row_0, rows = sg.rows;
+  __shared__ v4f lo[SPREAD ? kAttnWaves : 1][64];
+  __shared__ v2f lml[SPREAD ? kAttnWaves : 1][64];
 
-  for (int n = wave; n < kAcc; n += 4) {
+  for (int n = SPREAD ? (int)blockIdx.y : wave; n < kAcc; n += SPREAD ? kAcc : kAttnWaves) {
     const int r = n / kJ, j = n % kJ;
-    const uint32_t row = row_0 + 16 * r + col;
-    if (row >= rows || col >= ROWS) continue;
+    const uint32_t row = sp.row_0 + 16 * r + col;
+    const bool there = row < sp.rows && col < ROWS;
     float M = kUnset, Ls = 0.f;
     v4f o = {0.f, 0.f, 0.f, 0.f};
-    for (uint32_t w = blockIdx.x; w <= wl; ++w) {
-      const uint32_t x = attn_place(w, s0, share);
-      const v2f ml = *piece_ml<kRows>(a, x, 16 * r + col);
-      const v4f po = *piece_o<kAcc, kRows>(a, x, n, lane);
-      const float m = fmaxf(M, ml[0]), f0 = exp2_hw(M - m), f1 = exp2_hw(ml[0] - m);
-      o = o * f0 + po * f1;
-      Ls = Ls * f0 + ml[1] * f1;
-      M = m;
+    if (there) {
+#pragma unroll 4
+      for (uint32_t w = SPREAD ? wave : 0; w <= sp.followers; w += SPREAD ? kAttnWaves : 1) {
+        const uint32_t x = attn_place(blockIdx.x + w, w == 0);
+        const v2f ml = *piece_ml<ROWS>(a, x, 16 * r + col);
+        const v4f po = *piece_o<kAcc, ROWS>(a, x, n, lane);
+        const float m = fmaxf(M, ml[0]), f0 = exp2_hw(M - m), f1 = exp2_hw(ml[0] - m);
+        o = o * f0 + po * f1;
+        Ls = Ls * f0 + ml[1] * f1;
+        M = m;
+      }
     }
+    if constexpr (SPREAD) {
+      lo[wave][lane] = o;
+      lml[wave][lane] = v2f{M, Ls};
+      __syncthreads();
+      if (wave != 0) return;
+#pragma unroll
+      for (int w = 1; w < kAttnWaves; ++w) {
+        const v2f ml = lml[w][lane];
+        const float m = fmaxf(M, ml[0]), f0 = exp2_hw(M - m), f1 = exp2_hw(ml[0] - m);
+        o = o * f0 + lo[w][lane] * f1;
+        Ls = Ls * f0 + ml[1] * f1;
+        M = m;
+      }
+    }
+    if (!there) continue;
     const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
-    const int64_t orow = out_row(a, sq, sg.h, row);
+    const int64_t orow = out_row(a, sp.row0, sp.h, row);
     uint16_t* out = static_cast<uint16_t*>(a.out) + orow * D;
 #pragma unroll
     for (int i = 0; i < 4; ++i) out[(4 * g + i) * kJ + j] = (uint16_t)to16<FP16>(o[i] * inv, 0.f);
@@ -832,7 +869,14 @@ hipError_t attn_go(const AttnArgs& a, hipStream_t st) {
   hipLaunchKernelGGL((k_attn<FP16, D, BITS, ROWS>), dim3((unsigned)a.workgroups), dim3(64 * kAttnWaves), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.workgroups == 1) return e;
-  hipLaunchKernelGGL((k_attn_join<FP16, D, ROWS>), dim3((unsigned)a.workgroups - 1), dim3(256), 0, st, a);
+  // many pieces to a segment where there are few segments
+  const int64_t segments = (int64_t)a.sh.B * a.sh.Hkv * attn_row_tiles(a.sh.max_q, a.sh.G, ROWS);
+  const dim3 wg(64 * kAttnWaves);
+  if (segments * 4 <= a.workgroups)
+    hipLaunchKernelGGL((k_attn_join<FP16, D, ROWS, true>),
+                       dim3((unsigned)a.workgroups - 1, (ROWS > 16 ? ROWS / 16 : 1) * D / 16), wg, 0, st, a);
+  else
+    hipLaunchKernelGGL((k_attn_join<FP16, D, ROWS, false>), dim3((unsigned)a.workgroups - 1), wg, 0, st, a);
   return hipGetLastError();
 }
 
@@ -863,8 +907,10 @@ int64_t attn_workspace(AttnArgs* a, int64_t D, void* ws) {
   const int64_t pieces = 2 * (int64_t)a->workgroups, kept = a->sh.rows < 16 ? 16 : a->sh.rows;
   const int64_t o = pieces * kept * D * 4;
   a->part = static_cast<float*>(ws);
+  const int64_t ml = o + pieces * kept * 8;
   a->part_ml = ws ? reinterpret_cast<float*>(static_cast<char*>(ws) + o) : nullptr;
-  return o + pieces * kept * 8;
+  a->splits = ws ? static_cast<char*>(ws) + ml : nullptr;
+  return ml + (int64_t)a->workgroups * sizeof(AttnSplit);
 }
 
 hipError_t launch_attn(const AttnArgs& a, bool fp16, int bits, int D, hipStream_t st) {

@@ -5,10 +5,11 @@
 // A segment is one row tile (rows are query token x query head of a key head's
 // group) of one key head of one sequence; it holds the sequence's tiles of 32
 // cached tokens.  Segments lie one behind the other (sequence, key head, row
-// tile), and their tiles, counted through, are the units of work.  Workgroup w
-// takes units [w share, (w + 1) share): whole segments, and pieces of those
-// that straddle its borders.  All but the first and the last of its segments
-// are whole, so a workgroup leaves two pieces at most.
+// tile), each as kAttnStart units for its beginning and end (loads that wait
+// for loads, the join of the waves) and a unit per tile.  Workgroup w takes
+// units [w share, (w + 1) share): whole segments, and pieces of those that
+// straddle its borders: the end of one that began before, and the beginning of
+// one that goes on.
 #pragma once
 
 #include <stdint.h>
@@ -24,6 +25,7 @@ namespace w8 {
 
 constexpr int kAttnTile = 32;     // cached tokens to a unit
 constexpr int kAttnWaves = 4;     // waves to a workgroup, each with a part of its tiles
+constexpr uint32_t kAttnStart = 6;   // units that a segment counts for beside its tiles
 
 struct AttnShape {
   int B, T, Hkv, G, max_q, page, max_pages, causal;
@@ -58,7 +60,7 @@ W8_HD uint32_t attn_row_tiles(int n, int G, int rows) {
 }
 
 W8_HD uint32_t attn_units(const AttnShape& a, const AttnSeq& s) {
-  return (uint32_t)a.Hkv * attn_row_tiles(s.n, a.G, a.rows) * attn_tiles(s.L);
+  return (uint32_t)a.Hkv * attn_row_tiles(s.n, a.G, a.rows) * (attn_tiles(s.L) + kAttnStart);
 }
 
 // Keys that query token i of the sequence sees.
@@ -77,26 +79,35 @@ W8_HD uint32_t attn_share(uint32_t total, uint32_t workgroups) {
 
 // The segment that holds unit u of a sequence (u and hi from the sequence's
 // first unit; units of the workgroup end before hi): the key head, the first
-// row and the rows there are, and its tiles from `first` to before `last`.
+// row and the rows there are, the units from u to its end or the workgroup's,
+// and the tiles among them, from `first` to before `last` of `tiles`.  Without
+// tiles (only units of the beginning) there is nothing to do.
 struct AttnSeg {
   int h;
-  uint32_t row_0, rows, tiles, first, last;
+  uint32_t row_0, rows, units, tiles, first, last;
 };
 W8_HD AttnSeg attn_segment(const AttnShape& a, const AttnSeq& s, uint32_t u, uint32_t hi) {
   AttnSeg g;
   g.tiles = attn_tiles(s.L);
-  const uint32_t nrt = attn_row_tiles(s.n, a.G, a.rows), seg = u / g.tiles;
-  g.first = u - seg * g.tiles;
-  g.last = hi - u < g.tiles - g.first ? g.first + (hi - u) : g.tiles;
+  const uint32_t each = g.tiles + kAttnStart, nrt = attn_row_tiles(s.n, a.G, a.rows), seg = u / each;
+  const uint32_t from = u - seg * each, to = hi - u < each - from ? from + (hi - u) : each;
+  g.units = to - from;
+  g.first = from > kAttnStart ? from - kAttnStart : 0;
+  g.last = to > kAttnStart ? to - kAttnStart : 0;
   g.h = (int)(seg / nrt);
   g.row_0 = (seg - (uint32_t)g.h * nrt) * (uint32_t)a.rows;
   g.rows = (uint32_t)s.n * (uint32_t)a.G;
   return g;
 }
 
-// The place of workgroup w's piece of a segment whose first unit is s0, when
-// others hold the rest: a workgroup's first segment has one place, the one that
-// it begins after it the other.
-W8_HD uint32_t attn_place(uint32_t w, uint32_t s0, uint32_t share) { return 2 * w + (s0 > w * share ? 1u : 0u); }
+// A segment of `tiles` tiles of which the workgroup that takes the first ends
+// with `last`: the workgroups that take the others, one behind the other.
+W8_HD uint32_t attn_followers(uint32_t tiles, uint32_t last, uint32_t share) {
+  return (tiles - last + share - 1) / share;
+}
+
+// The place of a workgroup's piece of a segment that it shares with others:
+// one for the segment that it begins, one for the segment that began before.
+W8_HD uint32_t attn_place(uint32_t workgroup, bool begins) { return 2 * workgroup + (begins ? 1u : 0u); }
 
 }  // namespace w8

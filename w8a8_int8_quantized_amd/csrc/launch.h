@@ -138,7 +138,7 @@ hipError_t launch_kv(KvArgs a, bool write, int dtype, int bits, int D, hipStream
 
 // Attention over that cache (attn.hip); q_starts and lse may be null.
 // attn_workspace gives the workspace's size from a->sh and sets what depends
-// on it (part and part_ml in ws, the row tile, the grid).
+// on it (part, part_ml and splits in ws, the row tile, the grid).
 struct AttnArgs {
   const void* q;
   int64_t q_stride;
@@ -147,6 +147,7 @@ struct AttnArgs {
   const int32_t *table, *kv_lens, *q_starts;
   void* out;
   float *lse, *part, *part_ml;
+  void* splits;
   AttnShape sh;
   int pages, workgroups;
   float scale_log2;               // scale * log2(e)
