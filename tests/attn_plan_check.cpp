@@ -33,7 +33,7 @@ int main() {
     a.B = pick(1, round % 3 ? 9 : 70);
     a.Hkv = pick(1, 5);
     a.G = pick(1, 9);
-    a.rows = pick(0, 1) ? 16 : 32;
+    a.rows = 4 << pick(0, 4);
     a.page = 16 * pick(1, 6);
     a.max_pages = pick(0, 30);
     a.causal = pick(0, 1);

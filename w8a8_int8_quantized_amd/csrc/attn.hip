@@ -200,6 +200,11 @@ struct Attn {
   static constexpr int kRows = ROWS;
   static constexpr int kRegs = R * kJ * 4;          // accumulator registers of a lane
   static constexpr int kRound = 8;                  // accumulators (of 4) per round through LDS
+  // With more than one row fragment the query operand and the accumulators'
+  // starting values lie in LDS, one copy to the workgroup: the registers hold
+  // the accumulators of up to 64 rows of 128 channels instead.
+  static constexpr bool kQueryLds = R > 1;
+  static constexpr int kQueryBytes = kQueryLds ? R * (kSteps + 1) * 1024 : 0;
   using KC = KeyCodes<FP16, BITS>;
 
   // A tile in LDS: the half tiles' keys and values (16 tokens each), 4 x 16 kDB
@@ -327,20 +332,34 @@ struct Attn {
     }
   }
 
-  // The scores of a tile in codes.
+  // The scores of a tile in codes.  qf: the query operand in registers, or in
+  // LDS (ql, at the lane's place).
   static __device__ __forceinline__ void scores(const uint8_t* tile, const Lane& l, const v4u (*qf)[kSteps],
-                                                const float* c0, const Exponents& e, v4f (*s)[2]) {
+                                                const uint8_t* ql, const float* c0, const Exponents& e, v4f (*s)[2]) {
+    if constexpr (kQueryLds) {
+      uint32_t w[2][kW];
+      keys(tile, l, 0, w[0]);
+      keys(tile, l, 1, w[1]);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t w[kW];
-      keys(tile, l, h, w);
-#pragma unroll
-      for (int r = 0; r < R; ++r) s[r][h] = v4f{c0[r], c0[r], c0[r], c0[r]};
+      for (int r = 0; r < R; ++r) s[r][0] = s[r][1] = *reinterpret_cast<const v4f*>(ql + (R * kSteps + r) * 1024);
 #pragma unroll
       for (int j = 0; j < kSteps; ++j) {
-        const v4u ko = KC::operand(w + j * (BITS / 4), e.key);
+        const v4u k0 = KC::operand(w[0] + j * (BITS / 4), e.key), k1 = KC::operand(w[1] + j * (BITS / 4), e.key);
 #pragma unroll
-        for (int r = 0; r < R; ++r) s[r][h] = mma(ko, qf[r][j], s[r][h]);
+        for (int r = 0; r < R; ++r) {
+          const v4u q = *reinterpret_cast<const v4u*>(ql + (r * kSteps + j) * 1024);
+          s[r][0] = mma(k0, q, s[r][0]);
+          s[r][1] = mma(k1, q, s[r][1]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[kW];
+        keys(tile, l, h, w);
+        s[0][h] = v4f{c0[0], c0[0], c0[0], c0[0]};
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) s[0][h] = mma(KC::operand(w + j * (BITS / 4), e.key), qf[0][j], s[0][h]);
       }
     }
   }
@@ -592,6 +611,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_attn(AttnArgs a) {
   constexpr int R = A::R;
   __shared__ __align__(16) uint8_t ring[A::kLdsBytes];
   float* const lds = reinterpret_cast<float*>(ring);
+  __shared__ __align__(16) uint8_t query[A::kQueryLds ? A::kQueryBytes : 16];
   __shared__ float ldm[kAttnWaves][A::kRows], ldl[kAttnWaves][A::kRows];
   __shared__ uint32_t red[kAttnWaves + kAttnFound];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -656,7 +676,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_attn(AttnArgs a) {
 #pragma unroll
       for (int j = 0; j < A::kSteps; ++j) {
         qf[r][j] = v4u{0u, 0u, 0u, 0u};
-        if (row < rows && col < ROWS && t0 < t1) qf[r][j] = *reinterpret_cast<const v4u*>(src + 8 * j);
+        if (row < rows && col < ROWS && (A::kQueryLds || t0 < t1)) qf[r][j] = *reinterpret_cast<const v4u*>(src + 8 * j);
       }
     }
     wait_loads<0>();                  // only the tiles' loads are counted from here on
@@ -709,6 +729,18 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_attn(AttnArgs a) {
 #pragma unroll
       for (int j = 0; j < A::kJ; ++j) st.o[r][j] = v4f{0.f, 0.f, 0.f, 0.f};
     }
+    const uint8_t* const ql = query + 16 * lane;
+    if constexpr (A::kQueryLds) {
+      // (every wave has all of it, for c0)
+#pragma unroll
+      for (int i = 0; i < R * A::kSteps; ++i)
+        if (i % kAttnWaves == wave) *reinterpret_cast<v4u*>(query + 1024 * i + 16 * lane) = qf[i / A::kSteps][i % A::kSteps];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r % kAttnWaves == wave)
+          *reinterpret_cast<v4f*>(query + 1024 * (R * A::kSteps + r) + 16 * lane) = v4f{c0[r], c0[r], c0[r], c0[r]};
+      __syncthreads();
+    }
     for (uint32_t t = t0; t < t1; ++t) {
       // the loads of the tiles behind this one may be outstanding
       const uint32_t behind = t1 - 1 - t;
@@ -719,7 +751,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_attn(AttnArgs a) {
       const uint8_t* tile = mine + got;
       v4f s[R][2];
       v4u pf[R];
-      A::scores(tile, ln, qf, c0, e, s);
+      A::scores(tile, ln, qf, ql, c0, e, s);
       A::softmax(tile, ln, s, a.scale_log2, (int)t * kAttnTile, (int)(t + 1) * kAttnTile <= seen_least, sq.L, seen,
                  st, pf);
       uint32_t w[2][A::kW];
@@ -886,8 +918,9 @@ hipError_t attn_rows(const AttnArgs& a, hipStream_t st) {
     case 4: return attn_go<FP16, D, BITS, 4>(a, st);
     case 8: return attn_go<FP16, D, BITS, 8>(a, st);
     case 16: return attn_go<FP16, D, BITS, 16>(a, st);
+    case 32: return attn_go<FP16, D, BITS, 32>(a, st);
     default:
-      if constexpr (D < 256) return attn_go<FP16, D, BITS, 32>(a, st);
+      if constexpr (D < 256) return attn_go<FP16, D, BITS, 64>(a, st);
       return hipErrorInvalidValue;
   }
 }
@@ -902,8 +935,8 @@ hipError_t attn_pick(const AttnArgs& a, int bits, hipStream_t st) {
 // Rows to a row tile, workgroups and workspace of a call.
 int64_t attn_workspace(AttnArgs* a, int64_t D, void* ws) {
   const int64_t rows = (int64_t)a->sh.max_q * a->sh.G;
-  a->sh.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 || D == 256 ? 16 : 32;
-  a->workgroups = 512;
+  a->sh.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 || D == 256 ? 32 : 64;
+  a->workgroups = a->sh.rows > 16 ? 1024 : 512;
   const int64_t pieces = 2 * (int64_t)a->workgroups, kept = a->sh.rows < 16 ? 16 : a->sh.rows;
   const int64_t o = pieces * kept * D * 4;
   a->part = static_cast<float*>(ws);

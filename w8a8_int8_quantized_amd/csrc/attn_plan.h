@@ -25,7 +25,7 @@ namespace w8 {
 
 constexpr int kAttnTile = 32;     // cached tokens to a unit
 constexpr int kAttnWaves = 4;     // waves to a workgroup, each with a part of its tiles
-constexpr uint32_t kAttnStart = 6;   // units that a segment counts for beside its tiles
+constexpr uint32_t kAttnStart = 16;   // units that a segment counts for beside its tiles
 
 struct AttnShape {
   int B, T, Hkv, G, max_q, page, max_pages, causal;
