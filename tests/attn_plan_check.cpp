@@ -79,11 +79,15 @@ int main() {
           ++b;
           continue;
         }
-        const AttnSeg g = attn_segment(a, seq[b], u - base[b], hi - base[b]);
+        const AttnSeg g = attn_segment(a, seq[b], attn_head(a, seq[b]), u - base[b], hi - base[b]);
         CHECK(g.units > 0 && u + g.units <= hi);
         u += g.units;
         CHECK(g.h >= 0 && g.h < a.Hkv && g.row_0 < g.rows && g.first <= g.last && g.last <= g.tiles);
         if (g.first == g.last) continue;
+        // as many tiles as the last row sees
+        const uint32_t last_row = g.row_0 + (uint32_t)a.rows < g.rows ? g.row_0 + (uint32_t)a.rows - 1 : g.rows - 1;
+        const int most = attn_seen(a, seq[b], (int)(last_row / (uint32_t)a.G));
+        CHECK((int)g.tiles == (most > 0 ? (most + 31) / 32 : 1));
         const Segment s(b, g.h, g.row_0);
         auto& t = taken[s];
         t.resize(g.tiles);
@@ -99,7 +103,7 @@ int main() {
       }
     }
     uint32_t segments = 0;
-    for (int b = 0; b < a.B; ++b) segments += (uint32_t)a.Hkv * attn_row_tiles(seq[b].n, a.G, a.rows);
+    for (int b = 0; b < a.B; ++b) segments += (uint32_t)a.Hkv * attn_head(a, seq[b]).row_tiles;
     CHECK(taken.size() == segments);
     for (auto& t : taken)
       for (int n : t.second) CHECK(n == 1);

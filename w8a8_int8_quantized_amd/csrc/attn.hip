@@ -344,12 +344,16 @@ struct Attn {
       for (int r = 0; r < R; ++r) s[r][0] = s[r][1] = *reinterpret_cast<const v4f*>(ql + (R * kSteps + r) * 1024);
 #pragma unroll
       for (int j = 0; j < kSteps; ++j) {
+        // all fragments' operands are on their way before the codes are taken apart
+        v4u q[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) q[r] = *reinterpret_cast<const v4u*>(ql + (r * kSteps + j) * 1024);
+        __builtin_amdgcn_sched_barrier(0);
         const v4u k0 = KC::operand(w[0] + j * (BITS / 4), e.key), k1 = KC::operand(w[1] + j * (BITS / 4), e.key);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          const v4u q = *reinterpret_cast<const v4u*>(ql + (r * kSteps + j) * 1024);
-          s[r][0] = mma(k0, q, s[r][0]);
-          s[r][1] = mma(k1, q, s[r][1]);
+          s[r][0] = mma(k0, q[r], s[r][0]);
+          s[r][1] = mma(k1, q[r], s[r][1]);
         }
       }
     } else {
@@ -631,26 +635,25 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_attn(AttnArgs a) {
   uint32_t base = f.base;
   AttnSeq sq = f.sq;
   for (uint32_t u = lo; u < hi;) {
-    const uint32_t units = attn_units(a.sh, sq);
+    const AttnHead hd = attn_head(a.sh, sq);
+    const uint32_t units = (uint32_t)a.sh.Hkv * hd.units;
     if (u >= base + units) {
       base += units;
       sq = get_seq(a, ++b);
       continue;
     }
-    const AttnSeg sg = attn_segment(a.sh, sq, u - base, hi - base);
+    const AttnSeg sg = attn_segment(a.sh, sq, hd, u - base, hi - base);
     u += sg.units;
     if (sg.first == sg.last) continue;
     const uint32_t tiles = sg.tiles, first = sg.first, last = sg.last, row_0 = sg.row_0, rows = sg.rows;
     const int h = sg.h;
-    const uint32_t row_last = row_0 + A::kRows < rows ? row_0 + A::kRows - 1 : rows - 1;
-    // tiles that the last row sees, and tokens that the first does
-    const int seen_most = attn_seen(a.sh, sq, (int)(row_last / (uint32_t)a.sh.G));
+    // the tokens that the first row sees, and all others then; tiles that see nothing are not computed
     const int seen_least = attn_seen(a.sh, sq, (int)(row_0 / (uint32_t)a.sh.G));
-    const uint32_t end_seen = (uint32_t)(seen_most + kAttnTile - 1) / kAttnTile;
-    const uint32_t end = last < end_seen ? last : end_seen;
-    const uint32_t count = end > first ? end - first : 0;
+    const uint32_t row_last = row_0 + A::kRows < rows ? row_0 + A::kRows - 1 : rows - 1;
+    const bool nothing = attn_seen(a.sh, sq, (int)(row_last / (uint32_t)a.sh.G)) == 0;
+    const uint32_t count = nothing ? 0 : last - first;
     const uint32_t per = (count + kAttnWaves - 1) / kAttnWaves;
-    const uint32_t t0 = first + wave * per, t1 = t0 + per < end ? t0 + per : end;
+    const uint32_t t0 = first + wave * per, end = first + count, t1 = t0 + per < end ? t0 + per : end;
 
     // The wave's tiles one behind the other, in half tiles of 16 tokens (which
     // lie in one page).  The pages are in a register, 64 at a time: a page id
@@ -854,46 +857,45 @@ __global__ __launch_bounds__(64 * kAttnWaves) void k_attn_join(AttnArgs a) {
   __shared__ v4f lo[SPREAD ? kAttnWaves : 1][64];
   __shared__ v2f lml[SPREAD ? kAttnWaves : 1][64];
 
-  for (int n = SPREAD ? (int)blockIdx.y : wave; n < kAcc; n += SPREAD ? kAcc : kAttnWaves) {
-    const int r = n / kJ, j = n % kJ;
-    const uint32_t row = sp.row_0 + 16 * r + col;
-    const bool there = row < sp.rows && col < ROWS;
-    float M = kUnset, Ls = 0.f;
-    v4f o = {0.f, 0.f, 0.f, 0.f};
-    if (there) {
+  const int n = SPREAD ? (int)blockIdx.y : (int)blockIdx.y * kAttnWaves + wave;
+  const int r = n / kJ, j = n % kJ;
+  const uint32_t row = sp.row_0 + 16 * r + col;
+  const bool there = row < sp.rows && col < ROWS;
+  float M = kUnset, Ls = 0.f;
+  v4f o = {0.f, 0.f, 0.f, 0.f};
+  if (there) {
 #pragma unroll 4
-      for (uint32_t w = SPREAD ? wave : 0; w <= sp.followers; w += SPREAD ? kAttnWaves : 1) {
-        const uint32_t x = attn_place(blockIdx.x + w, w == 0);
-        const v2f ml = *piece_ml<ROWS>(a, x, 16 * r + col);
-        const v4f po = *piece_o<kAcc, ROWS>(a, x, n, lane);
-        const float m = fmaxf(M, ml[0]), f0 = exp2_hw(M - m), f1 = exp2_hw(ml[0] - m);
-        o = o * f0 + po * f1;
-        Ls = Ls * f0 + ml[1] * f1;
-        M = m;
-      }
+    for (uint32_t w = SPREAD ? wave : 0; w <= sp.followers; w += SPREAD ? kAttnWaves : 1) {
+      const uint32_t x = attn_place(blockIdx.x + w, w == 0);
+      const v2f ml = *piece_ml<ROWS>(a, x, 16 * r + col);
+      const v4f po = *piece_o<kAcc, ROWS>(a, x, n, lane);
+      const float m = fmaxf(M, ml[0]), f0 = exp2_hw(M - m), f1 = exp2_hw(ml[0] - m);
+      o = o * f0 + po * f1;
+      Ls = Ls * f0 + ml[1] * f1;
+      M = m;
     }
-    if constexpr (SPREAD) {
-      lo[wave][lane] = o;
-      lml[wave][lane] = v2f{M, Ls};
-      __syncthreads();
-      if (wave != 0) return;
-#pragma unroll
-      for (int w = 1; w < kAttnWaves; ++w) {
-        const v2f ml = lml[w][lane];
-        const float m = fmaxf(M, ml[0]), f0 = exp2_hw(M - m), f1 = exp2_hw(ml[0] - m);
-        o = o * f0 + lo[w][lane] * f1;
-        Ls = Ls * f0 + ml[1] * f1;
-        M = m;
-      }
-    }
-    if (!there) continue;
-    const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
-    const int64_t orow = out_row(a, sp.row0, sp.h, row);
-    uint16_t* out = static_cast<uint16_t*>(a.out) + orow * D;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) out[(4 * g + i) * kJ + j] = (uint16_t)to16<FP16>(o[i] * inv, 0.f);
-    if (a.lse && j == 0 && g == 0) a.lse[orow] = log_sum(M, Ls);
   }
+  if constexpr (SPREAD) {
+    lo[wave][lane] = o;
+    lml[wave][lane] = v2f{M, Ls};
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int w = 1; w < kAttnWaves; ++w) {
+      const v2f ml = lml[w][lane];
+      const float m = fmaxf(M, ml[0]), f0 = exp2_hw(M - m), f1 = exp2_hw(ml[0] - m);
+      o = o * f0 + lo[w][lane] * f1;
+      Ls = Ls * f0 + ml[1] * f1;
+      M = m;
+    }
+  }
+  if (!there) return;
+  const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+  const int64_t orow = out_row(a, sp.row0, sp.h, row);
+  uint16_t* out = static_cast<uint16_t*>(a.out) + orow * D;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) out[(4 * g + i) * kJ + j] = (uint16_t)to16<FP16>(o[i] * inv, 0.f);
+  if (a.lse && j == 0 && g == 0) a.lse[orow] = log_sum(M, Ls);
 }
 
 template <bool FP16, int D, int BITS, int ROWS>
@@ -902,13 +904,14 @@ hipError_t attn_go(const AttnArgs& a, hipStream_t st) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.workgroups == 1) return e;
   // many pieces to a segment where there are few segments
-  const int64_t segments = (int64_t)a.sh.B * a.sh.Hkv * attn_row_tiles(a.sh.max_q, a.sh.G, ROWS);
+  const int64_t segments = (int64_t)a.sh.B * a.sh.Hkv * (((int64_t)a.sh.max_q * a.sh.G + ROWS - 1) / ROWS);
+  constexpr int kAcc = (ROWS > 16 ? ROWS / 16 : 1) * D / 16;
   const dim3 wg(64 * kAttnWaves);
   if (segments * 4 <= a.workgroups)
     hipLaunchKernelGGL((k_attn_join<FP16, D, ROWS, true>),
-                       dim3((unsigned)a.workgroups - 1, (ROWS > 16 ? ROWS / 16 : 1) * D / 16), wg, 0, st, a);
+                       dim3((unsigned)a.workgroups - 1, kAcc), wg, 0, st, a);
   else
-    hipLaunchKernelGGL((k_attn_join<FP16, D, ROWS, false>), dim3((unsigned)a.workgroups - 1), wg, 0, st, a);
+    hipLaunchKernelGGL((k_attn_join<FP16, D, ROWS, false>), dim3((unsigned)a.workgroups - 1, kAcc / kAttnWaves), wg, 0, st, a);
   return hipGetLastError();
 }
 
@@ -936,7 +939,7 @@ hipError_t attn_pick(const AttnArgs& a, int bits, hipStream_t st) {
 int64_t attn_workspace(AttnArgs* a, int64_t D, void* ws) {
   const int64_t rows = (int64_t)a->sh.max_q * a->sh.G;
   a->sh.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 || D == 256 ? 32 : 64;
-  a->workgroups = a->sh.rows > 16 ? 1024 : 512;
+  a->workgroups = 512;
   const int64_t pieces = 2 * (int64_t)a->workgroups, kept = a->sh.rows < 16 ? 16 : a->sh.rows;
   const int64_t o = pieces * kept * D * 4;
   a->part = static_cast<float*>(ws);

@@ -3,13 +3,19 @@
 // checks them on the CPU.
 //
 // A segment is one row tile (rows are query token x query head of a key head's
-// group) of one key head of one sequence; it holds the sequence's tiles of 32
-// cached tokens.  Segments lie one behind the other (sequence, key head, row
-// tile), each as kAttnStart units for its beginning and end (loads that wait
-// for loads, the join of the waves) and a unit per tile.  Workgroup w takes
-// units [w share, (w + 1) share): whole segments, and pieces of those that
-// straddle its borders: the end of one that began before, and the beginning of
-// one that goes on.
+// group) of one key head of one sequence; it holds the tiles of 32 cached
+// tokens that its rows see.  Segments lie one behind the other (sequence, key
+// head, row tile), each as kAttnStart units for its beginning and end (loads
+// that wait for loads, the join of the waves) and a unit per tile.  Workgroup w
+// takes units [w share, (w + 1) share): whole segments, and pieces of those
+// that straddle its borders: the end of one that began before, and the
+// beginning of one that goes on.
+//
+// With causal masks later row tiles see more.  A head's row tiles lie in pairs
+// (the last with the first, the last but one with the second, ..), whose tiles
+// add up to nearly the same for all: a pair has a fixed number of units, the
+// few that its two segments leave are empty, and so the place of every segment
+// follows by division.
 #pragma once
 
 #include <stdint.h>
@@ -49,26 +55,45 @@ W8_HD AttnSeq attn_seq(const AttnShape& a, int q0, int q1, int len) {
   return s;
 }
 
-// Tiles of a sequence; one without cached tokens has a tile too, which holds
-// nothing and gives its rows their zeros.
-W8_HD uint32_t attn_tiles(int L) {
-  return L > 0 ? (uint32_t)(L + kAttnTile - 1) / kAttnTile : 1u;
-}
-
-W8_HD uint32_t attn_row_tiles(int n, int G, int rows) {
-  return (uint32_t)(((int64_t)n * G + rows - 1) / rows);
-}
-
-W8_HD uint32_t attn_units(const AttnShape& a, const AttnSeq& s) {
-  return (uint32_t)a.Hkv * attn_row_tiles(s.n, a.G, a.rows) * (attn_tiles(s.L) + kAttnStart);
-}
-
 // Keys that query token i of the sequence sees.
 W8_HD int attn_seen(const AttnShape& a, const AttnSeq& s, int i) {
   if (!a.causal) return s.L;
   const int64_t k = (int64_t)s.L - s.n + i + 1;
   return k < 0 ? 0 : (int)k;
 }
+
+// Tiles that row tile rt sees; one that sees nothing has a tile too, which
+// gives its rows their zeros.
+W8_HD uint32_t attn_tiles(const AttnShape& a, const AttnSeq& s, uint32_t rt) {
+  const int64_t last = ((int64_t)(rt + 1) * a.rows - 1) / a.G;
+  const int seen = attn_seen(a, s, last < s.n ? (int)last : s.n - 1);
+  return seen > 0 ? (uint32_t)(seen + kAttnTile - 1) / kAttnTile : 1u;
+}
+
+// A key head of a sequence: its row tiles, the units of a pair of them, and
+// all its units.
+struct AttnHead {
+  uint32_t row_tiles, pair, units;
+};
+W8_HD AttnHead attn_head(const AttnShape& a, const AttnSeq& s) {
+  AttnHead h;
+  h.row_tiles = (uint32_t)(((int64_t)s.n * a.G + a.rows - 1) / a.rows);
+  h.pair = 0;
+  if (h.row_tiles > 1) {
+    if (a.causal && s.L >= s.n) {
+      // the last tokens of row tiles k and row_tiles - 1 - k add up to `most` at most
+      const int64_t most = 2 * (int64_t)(s.L - s.n) + ((int64_t)(h.row_tiles + 1) * a.rows - 2) / a.G + 2;
+      h.pair = (uint32_t)((most + 2 * kAttnTile - 2) / kAttnTile);
+    } else {
+      h.pair = 2 * attn_tiles(a, s, h.row_tiles - 1);
+    }
+    h.pair += 2 * kAttnStart;
+  }
+  h.units = h.row_tiles / 2 * h.pair;
+  if (h.row_tiles & 1) h.units += kAttnStart + attn_tiles(a, s, h.row_tiles / 2);
+  return h;
+}
+W8_HD uint32_t attn_units(const AttnShape& a, const AttnSeq& s) { return (uint32_t)a.Hkv * attn_head(a, s).units; }
 
 // Units to a workgroup: an even share, but two tiles to a wave at least.
 W8_HD uint32_t attn_share(uint32_t total, uint32_t workgroups) {
@@ -81,22 +106,44 @@ W8_HD uint32_t attn_share(uint32_t total, uint32_t workgroups) {
 // first unit; units of the workgroup end before hi): the key head, the first
 // row and the rows there are, the units from u to its end or the workgroup's,
 // and the tiles among them, from `first` to before `last` of `tiles`.  Without
-// tiles (only units of the beginning) there is nothing to do.
+// tiles (only units of a beginning, or empty ones) there is nothing to do.
 struct AttnSeg {
   int h;
   uint32_t row_0, rows, units, tiles, first, last;
 };
-W8_HD AttnSeg attn_segment(const AttnShape& a, const AttnSeq& s, uint32_t u, uint32_t hi) {
+W8_HD AttnSeg attn_segment(const AttnShape& a, const AttnSeq& s, const AttnHead& hd, uint32_t u, uint32_t hi) {
   AttnSeg g;
-  g.tiles = attn_tiles(s.L);
-  const uint32_t each = g.tiles + kAttnStart, nrt = attn_row_tiles(s.n, a.G, a.rows), seg = u / each;
-  const uint32_t from = u - seg * each, to = hi - u < each - from ? from + (hi - u) : each;
+  const uint32_t h = u / hd.units, v = u - h * hd.units, left = hi - u;
+  const uint32_t k = hd.pair ? v / hd.pair : 0;
+  uint32_t from = v, rt = hd.row_tiles / 2;
+  g.h = (int)h;
+  g.rows = (uint32_t)s.n * (uint32_t)a.G;
+  bool second = false;
+  if (k < hd.row_tiles / 2) {
+    rt = hd.row_tiles - 1 - k;
+    from = v - k * hd.pair;
+    const uint32_t longer = kAttnStart + attn_tiles(a, s, rt);
+    if (from >= longer) {
+      rt = k;
+      from -= longer;
+      second = true;
+    }
+  } else {
+    from = v - hd.row_tiles / 2 * hd.pair;
+  }
+  g.tiles = attn_tiles(a, s, rt);
+  g.row_0 = rt * (uint32_t)a.rows;
+  const uint32_t each = kAttnStart + g.tiles;
+  if (second && from >= each) {   // the empty units of a pair
+    const uint32_t rest = (k + 1) * hd.pair - v;
+    g.units = rest < left ? rest : left;
+    g.first = g.last = 0;
+    return g;
+  }
+  const uint32_t to = left < each - from ? from + left : each;
   g.units = to - from;
   g.first = from > kAttnStart ? from - kAttnStart : 0;
   g.last = to > kAttnStart ? to - kAttnStart : 0;
-  g.h = (int)(seg / nrt);
-  g.row_0 = (seg - (uint32_t)g.h * nrt) * (uint32_t)a.rows;
-  g.rows = (uint32_t)s.n * (uint32_t)a.G;
   return g;
 }
 
