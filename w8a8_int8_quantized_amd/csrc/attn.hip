@@ -848,24 +848,24 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_attn(AttnArgs a) {
 // accumulator, whose waves take turns at the pieces and join in LDS; otherwise
 // a wave to every fourth accumulator, with all pieces in order.
 template <bool FP16, int D, int ROWS, bool SPREAD>
-__global__ __launch_bounds__(64 * kAttnWaves) void k_attn_join(AttnArgs a) {
-  constexpr int kJ = D / 16, kAcc = (ROWS > 16 ? ROWS / 16 : 1) * kJ;
+__global__ __launch_bounds__(SPREAD ? 512 : 256) void k_attn_join(AttnArgs a) {
+  constexpr int kJ = D / 16, kAcc = (ROWS > 16 ? ROWS / 16 : 1) * kJ, kWaves = SPREAD ? 8 : 4;
   const AttnSplit sp = static_cast<const AttnSplit*>(a.splits)[blockIdx.x];
   if (sp.followers == 0) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, col = lane & 15;
-  __shared__ v4f lo[SPREAD ? kAttnWaves : 1][64];
-  __shared__ v2f lml[SPREAD ? kAttnWaves : 1][64];
+  __shared__ v4f lo[SPREAD ? kWaves : 1][64];
+  __shared__ v2f lml[SPREAD ? kWaves : 1][64];
 
-  const int n = SPREAD ? (int)blockIdx.y : (int)blockIdx.y * kAttnWaves + wave;
+  const int n = SPREAD ? (int)blockIdx.y : (int)blockIdx.y * kWaves + wave;
   const int r = n / kJ, j = n % kJ;
   const uint32_t row = sp.row_0 + 16 * r + col;
   const bool there = row < sp.rows && col < ROWS;
   float M = kUnset, Ls = 0.f;
   v4f o = {0.f, 0.f, 0.f, 0.f};
   if (there) {
-#pragma unroll 4
-    for (uint32_t w = SPREAD ? wave : 0; w <= sp.followers; w += SPREAD ? kAttnWaves : 1) {
+#pragma unroll 8
+    for (uint32_t w = SPREAD ? wave : 0; w <= sp.followers; w += SPREAD ? kWaves : 1) {
       const uint32_t x = attn_place(blockIdx.x + w, w == 0);
       const v2f ml = *piece_ml<ROWS>(a, x, 16 * r + col);
       const v4f po = *piece_o<kAcc, ROWS>(a, x, n, lane);
@@ -881,7 +881,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void k_attn_join(AttnArgs a) {
     __syncthreads();
     if (wave != 0) return;
 #pragma unroll
-    for (int w = 1; w < kAttnWaves; ++w) {
+    for (int w = 1; w < kWaves; ++w) {
       const v2f ml = lml[w][lane];
       const float m = fmaxf(M, ml[0]), f0 = exp2_hw(M - m), f1 = exp2_hw(ml[0] - m);
       o = o * f0 + lo[w][lane] * f1;
@@ -906,12 +906,11 @@ hipError_t attn_go(const AttnArgs& a, hipStream_t st) {
   // many pieces to a segment where there are few segments
   const int64_t segments = (int64_t)a.sh.B * a.sh.Hkv * (((int64_t)a.sh.max_q * a.sh.G + ROWS - 1) / ROWS);
   constexpr int kAcc = (ROWS > 16 ? ROWS / 16 : 1) * D / 16;
-  const dim3 wg(64 * kAttnWaves);
   if (segments * 4 <= a.workgroups)
     hipLaunchKernelGGL((k_attn_join<FP16, D, ROWS, true>),
-                       dim3((unsigned)a.workgroups - 1, kAcc), wg, 0, st, a);
+                       dim3((unsigned)a.workgroups - 1, kAcc), dim3(512), 0, st, a);
   else
-    hipLaunchKernelGGL((k_attn_join<FP16, D, ROWS, false>), dim3((unsigned)a.workgroups - 1, kAcc / kAttnWaves), wg, 0, st, a);
+    hipLaunchKernelGGL((k_attn_join<FP16, D, ROWS, false>), dim3((unsigned)a.workgroups - 1, kAcc / 4), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
@@ -921,9 +920,9 @@ hipError_t attn_rows(const AttnArgs& a, hipStream_t st) {
     case 4: return attn_go<FP16, D, BITS, 4>(a, st);
     case 8: return attn_go<FP16, D, BITS, 8>(a, st);
     case 16: return attn_go<FP16, D, BITS, 16>(a, st);
-    case 32: return attn_go<FP16, D, BITS, 32>(a, st);
     default:
-      if constexpr (D < 256) return attn_go<FP16, D, BITS, 64>(a, st);
+      if constexpr (D < 256)
+        return a.sh.rows == 32 ? attn_go<FP16, D, BITS, 32>(a, st) : attn_go<FP16, D, BITS, 64>(a, st);
       return hipErrorInvalidValue;
   }
 }
@@ -935,15 +934,25 @@ hipError_t attn_pick(const AttnArgs& a, int bits, hipStream_t st) {
 
 }  // namespace
 
-// Rows to a row tile, workgroups and workspace of a call.
+// Rows to a row tile, workgroups and workspace of a call.  A larger tile takes
+// the codes apart for more rows at once, smaller ones are more and shorter
+// segments.  Measured, us with 16, 32 and 64 rows (query rows of the call in
+// brackets): 4 tokens of 8 requests (768) 21, 25, -; 64 tokens on 4000 (2048)
+// 28, 30, 40; 16 tokens of 8 requests (4096) 39, 38, 46; 256 tokens on 4000
+// (8192) 55, 52, 61; 16 tokens of 64 requests (32768) 105, 74, 75; prompts'
+// pieces and single tokens (53000) 224, 167, 164; 2048 tokens on 8192 (65536)
+// 592, 387, 315.  256 channels leave registers for 16 rows only: 4 tokens of
+// 64 requests (2560) 63, 92, -.
+// 512 workgroups: two to a CU stream as fast as four (64 sequences of 8192:
+// 107 us with 512, 112 with 1024), and leave half the pieces.
 int64_t attn_workspace(AttnArgs* a, int64_t D, void* ws) {
-  const int64_t rows = (int64_t)a->sh.max_q * a->sh.G;
-  a->sh.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 || D == 256 ? 32 : 64;
+  const int64_t rows = (int64_t)a->sh.max_q * a->sh.G, all = (int64_t)a->sh.T * a->sh.Hkv * a->sh.G;
+  a->sh.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 || D == 256 || all < 4096 ? 16 : rows <= 32 || all < 40000 ? 32 : 64;
   a->workgroups = 512;
-  const int64_t pieces = 2 * (int64_t)a->workgroups, kept = a->sh.rows < 16 ? 16 : a->sh.rows;
-  const int64_t o = pieces * kept * D * 4;
+  // (room for the largest tile of these heads: the size goes by them alone)
+  const int64_t pieces = 2 * (int64_t)a->workgroups, kept = rows <= 16 || D == 256 ? 16 : rows <= 32 ? 32 : 64;
+  const int64_t o = pieces * kept * D * 4, ml = o + pieces * kept * 8;
   a->part = static_cast<float*>(ws);
-  const int64_t ml = o + pieces * kept * 8;
   a->part_ml = ws ? reinterpret_cast<float*>(static_cast<char*>(ws) + o) : nullptr;
   a->splits = ws ? static_cast<char*>(ws) + ml : nullptr;
   return ml + (int64_t)a->workgroups * sizeof(AttnSplit);

@@ -5,7 +5,7 @@
 // A segment is one row tile (rows are query token x query head of a key head's
 // group) of one key head of one sequence; it holds the tiles of 32 cached
 // tokens that its rows see.  Segments lie one behind the other (sequence, key
-// head, row tile), each as kAttnStart units for its beginning and end (loads
+// head, row tile), each as attn_start units for its beginning and end (loads
 // that wait for loads, the join of the waves) and a unit per tile.  Workgroup w
 // takes units [w share, (w + 1) share): whole segments, and pieces of those
 // that straddle its borders: the end of one that began before, and the
@@ -31,7 +31,6 @@ namespace w8 {
 
 constexpr int kAttnTile = 32;     // cached tokens to a unit
 constexpr int kAttnWaves = 4;     // waves to a workgroup, each with a part of its tiles
-constexpr uint32_t kAttnStart = 16;   // units that a segment counts for beside its tiles
 
 struct AttnShape {
   int B, T, Hkv, G, max_q, page, max_pages, causal;
@@ -42,6 +41,11 @@ struct AttnShape {
 struct AttnSeq {
   int row0, n, L;
 };
+
+// Units that a segment counts for beside its tiles.  Measured: decode batches
+// of 64 sequences up to 16384 tokens 102, 98, 98 and 100 us with 8, 16, 24 and
+// 40 (111 with 2), prompts' pieces beside single tokens 203, 176, 167 and 166.
+W8_HD uint32_t attn_start(const AttnShape& a) { return a.rows > 16 ? 28u : 16u; }
 
 // From the values in the arrays, which the host has not seen: clamped to what
 // the call's shapes allow, so that nothing outside is read or written.
@@ -87,10 +91,10 @@ W8_HD AttnHead attn_head(const AttnShape& a, const AttnSeq& s) {
     } else {
       h.pair = 2 * attn_tiles(a, s, h.row_tiles - 1);
     }
-    h.pair += 2 * kAttnStart;
+    h.pair += 2 * attn_start(a);
   }
   h.units = h.row_tiles / 2 * h.pair;
-  if (h.row_tiles & 1) h.units += kAttnStart + attn_tiles(a, s, h.row_tiles / 2);
+  if (h.row_tiles & 1) h.units += attn_start(a) + attn_tiles(a, s, h.row_tiles / 2);
   return h;
 }
 W8_HD uint32_t attn_units(const AttnShape& a, const AttnSeq& s) { return (uint32_t)a.Hkv * attn_head(a, s).units; }
@@ -115,6 +119,7 @@ W8_HD AttnSeg attn_segment(const AttnShape& a, const AttnSeq& s, const AttnHead&
   AttnSeg g;
   const uint32_t h = u / hd.units, v = u - h * hd.units, left = hi - u;
   const uint32_t k = hd.pair ? v / hd.pair : 0;
+  const uint32_t start = attn_start(a);
   uint32_t from = v, rt = hd.row_tiles / 2;
   g.h = (int)h;
   g.rows = (uint32_t)s.n * (uint32_t)a.G;
@@ -122,7 +127,7 @@ W8_HD AttnSeg attn_segment(const AttnShape& a, const AttnSeq& s, const AttnHead&
   if (k < hd.row_tiles / 2) {
     rt = hd.row_tiles - 1 - k;
     from = v - k * hd.pair;
-    const uint32_t longer = kAttnStart + attn_tiles(a, s, rt);
+    const uint32_t longer = start + attn_tiles(a, s, rt);
     if (from >= longer) {
       rt = k;
       from -= longer;
@@ -133,7 +138,7 @@ W8_HD AttnSeg attn_segment(const AttnShape& a, const AttnSeq& s, const AttnHead&
   }
   g.tiles = attn_tiles(a, s, rt);
   g.row_0 = rt * (uint32_t)a.rows;
-  const uint32_t each = kAttnStart + g.tiles;
+  const uint32_t each = start + g.tiles;
   if (second && from >= each) {   // the empty units of a pair
     const uint32_t rest = (k + 1) * hd.pair - v;
     g.units = rest < left ? rest : left;
@@ -142,8 +147,8 @@ W8_HD AttnSeg attn_segment(const AttnShape& a, const AttnSeq& s, const AttnHead&
   }
   const uint32_t to = left < each - from ? from + left : each;
   g.units = to - from;
-  g.first = from > kAttnStart ? from - kAttnStart : 0;
-  g.last = to > kAttnStart ? to - kAttnStart : 0;
+  g.first = from > start ? from - start : 0;
+  g.last = to > start ? to - start : 0;
   return g;
 }
 

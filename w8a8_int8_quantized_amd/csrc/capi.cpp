@@ -583,7 +583,7 @@ int attn_kv_cache(const void* q, int dtype, int64_t q_stride, const void* k_cach
   if (B == 0 || T == 0 || max_q == 0) return W8_OK;
   // the units of work stay inside 32 bits whatever the arrays hold
   const int64_t row_tiles = (max_q * (Hq / Hkv) + 15) / 16, tiles = (max_pages * page_size + 31) / 32 + 1;
-  if (B > kMaxRows / Hkv || B * Hkv > kMaxRows / row_tiles || B * Hkv * row_tiles > kMaxRows / (tiles + w8::kAttnStart))
+  if (B > kMaxRows / Hkv || B * Hkv > kMaxRows / row_tiles || B * Hkv * row_tiles > kMaxRows / (tiles + 32))
     return W8_ERR_SHAPE;
   if (!q || !kv_lens || !out || !workspace || (max_pages > 0 && !block_table)) return W8_ERR_NULL;
   rc = check_kv_pointers(k_cache, k_scale, v_cache, v_scale);
