@@ -639,27 +639,45 @@ def kv_cache_empty(pages, kv_heads, page_size, head_dim, bits=4, device="cuda"):
 def _kv_cache(cache):
     """A cache's (bits, head_dim, pages, heads, page size, device), its arrays checked against each other."""
     k, ks, v, vs = cache
+    shape, dt, dev, f32 = k.shape, k.dtype, k.device, torch.float32
+    bits = 4 if dt is torch.uint8 else 8 if dt is torch.int8 else 0
+    if bits and len(shape) == 4 and k.is_cuda:
+        pages, H, page, db = shape
+        per_row = shape[:3]
+        # (one condition: the checks of a small call cost more than its kernels otherwise)
+        if (ks.shape == per_row and vs.shape == per_row and v.shape == (pages, H, page // 4, 16, 4, db // 16)
+                and v.dtype is dt and ks.dtype is f32 and vs.dtype is f32 and v.device == dev and ks.device == dev
+                and vs.device == dev and k.is_contiguous() and v.is_contiguous() and ks.is_contiguous()
+                and vs.is_contiguous()):
+            return bits, db * 8 // bits, pages, H, page, dev
+    # what is wrong with it
     _dev(k)
     _dims(k, "cache k", 4)
-    if k.dtype not in (torch.uint8, torch.int8):
-        raise W8Error(f"cache k must be uint8 (4 bits) or int8 (8 bits), got {k.dtype}")
-    pages, H, page, db = k.shape
-    dev = k.device
-    _like(ks, "cache k_scale", (pages, H, page), torch.float32, dev)
-    _like(v, "cache v", (pages, H, page // 4, 16, 4, db // 16), k.dtype, dev)
-    _like(vs, "cache v_scale", (pages, H, page), torch.float32, dev)
-    bits = 4 if k.dtype == torch.uint8 else 8
-    return bits, db * 8 // bits, pages, H, page, dev
+    if not bits:
+        raise W8Error(f"cache k must be uint8 (4 bits) or int8 (8 bits), got {dt}")
+    pages, H, page, db = shape
+    _like(ks, "cache k_scale", (pages, H, page), f32, dev)
+    _like(v, "cache v", (pages, H, page // 4, 16, 4, db // 16), dt, dev)
+    _like(vs, "cache v_scale", (pages, H, page), f32, dev)
+    raise W8Error("cache: unusable arrays")
 
 
 def _token_rows(t, name, shape, dtype, dev):
     """The stride between tokens of t [T, heads, D], whose heads and channels are contiguous."""
-    if t.shape != shape or t.dtype != dtype or t.device != dev:
+    if t.shape != shape or t.dtype is not dtype or t.device != dev:
         raise W8Error(f"{name} must be {dtype} {shape} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     T, H, D = shape
-    if t.numel() and (t.stride(2) != 1 or (H > 1 and t.stride(1) != D)):
+    if t.is_contiguous():
+        return H * D
+    between, head, one = t.stride()
+    if one != 1 or (H > 1 and head != D):
         raise W8Error(f"{name}: heads and channels must be contiguous")
-    return t.stride(0) if T > 1 else H * D
+    return between if T > 1 else H * D
+
+
+def _index(t, shape, dev):
+    """t is a contiguous int32 tensor of this shape on dev."""
+    return t.dtype is torch.int32 and t.shape == shape and t.device == dev and t.is_contiguous()
 
 
 def quant_kv_cache(k, v, slots, cache):
@@ -673,9 +691,11 @@ def quant_kv_cache(k, v, slots, cache):
     bits, D, pages, H, page, dev = _kv_cache(cache)
     _dims(k, "k", 3)
     T = k.shape[0]
-    k_stride = _token_rows(k, "k", (T, H, D), k.dtype, dev)
-    v_stride = _token_rows(v, "v", (T, H, D), k.dtype, dev)
-    _like(slots, "slots", (T,), torch.int32, dev)
+    shape, dt = (T, H, D), k.dtype
+    k_stride = _token_rows(k, "k", shape, dt, dev)
+    v_stride = _token_rows(v, "v", shape, dt, dev)
+    if not _index(slots, (T,), dev):
+        _like(slots, "slots", (T,), torch.int32, dev)
     kc, ks, vc, vs = cache
     _run_on(dev, "quant_kv_cache", lib.quant_kv_cache, k.data_ptr(), v.data_ptr(), _act_dtype(k), k_stride, v_stride,
             slots.data_ptr(), T, H, D, bits, pages, page, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr())
@@ -688,7 +708,8 @@ def dequant_kv_cache(cache, slots, dtype=torch.bfloat16, out=None):
     bits, D, pages, H, page, dev = _kv_cache(cache)
     _dims(slots, "slots", 1)
     T = slots.shape[0]
-    _like(slots, "slots", (T,), torch.int32, dev)
+    if not _index(slots, (T,), dev):
+        _like(slots, "slots", (T,), torch.int32, dev)
     if out is None:
         out = torch.empty(T, H, D, dtype=dtype, device=dev), torch.empty(T, H, D, dtype=dtype, device=dev)
     else:
@@ -729,13 +750,16 @@ def attn_kv_cache(q, cache, block_table, kv_lens, q_starts=None, max_q=None, sca
     """
     bits, D, pages, H, page, dev = _kv_cache(cache)
     _dims(q, "q", 3)
-    T, Hq = q.shape[0], q.shape[1]
-    code = _act_dtype(q)
-    stride = _token_rows(q, "q", (T, Hq, D), q.dtype, dev)
     _dims(block_table, "block_table", 2)
+    T, Hq, _ = q.shape
     B, max_pages = block_table.shape
-    _like(block_table, "block_table", (B, max_pages), torch.int32, dev)
-    _like(kv_lens, "kv_lens", (B,), torch.int32, dev)
+    dt, shape = q.dtype, (T, Hq, D)
+    code = _act_dtype(q)
+    stride = _token_rows(q, "q", shape, dt, dev)
+    if not _index(block_table, (B, max_pages), dev):
+        _like(block_table, "block_table", (B, max_pages), torch.int32, dev)
+    if not _index(kv_lens, (B,), dev):
+        _like(kv_lens, "kv_lens", (B,), torch.int32, dev)
     if q_starts is not None:
         _like(q_starts, "q_starts", (B + 1,), torch.int32, dev)
         max_q = T if max_q is None else min(max_q, T)
@@ -747,20 +771,26 @@ def attn_kv_cache(q, cache, block_table, kv_lens, q_starts=None, max_q=None, sca
     if Hq % H or not Hq:
         raise W8Error(f"attn_kv_cache: {Hq} query heads for {H} key/value heads")
     if out is None:
-        out = torch.empty(T, Hq, D, dtype=q.dtype, device=dev)
+        o = out = torch.empty(T, Hq, D, dtype=dt, device=dev)
+        z = None
         if lse:
-            out = out, torch.empty(T, Hq, dtype=torch.float32, device=dev)
-    elif lse:
-        _like(out[1], "out lse", (T, Hq), torch.float32, dev)
-    o, z = out if lse else (out, None)
-    _like(o, "out", (T, Hq, D), q.dtype, dev)
+            z = torch.empty(T, Hq, dtype=torch.float32, device=dev)
+            out = o, z
+    else:
+        o, z = out if lse else (out, None)
+        _like(o, "out", shape, dt, dev)
+        if lse:
+            _like(z, "out lse", (T, Hq), torch.float32, dev)
+    need = attn_workspace_bytes(max_q, Hq, H, D)
     if workspace is None:
-        workspace = torch.empty(attn_workspace_bytes(max_q, Hq, H, D), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise W8Error(f"workspace must be contiguous, on {dev}")
+    else:
+        need = workspace.numel() * workspace.element_size()
     kc, ks, vc, vs = cache
     _run_on(dev, "attn_kv_cache", lib.attn_kv_cache, q.data_ptr(), code, stride, kc.data_ptr(), ks.data_ptr(),
             vc.data_ptr(), vs.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), _ptr(q_starts), B, T, max_q, Hq,
             H, D, bits, pages, page, max_pages, D ** -0.5 if scale is None else scale, causal, o.data_ptr(), _ptr(z),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size())
+            workspace.data_ptr(), need)
     return out
