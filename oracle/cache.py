@@ -43,20 +43,21 @@ def put(cache, page, place, head, kq, ks, vq, vs, bits):
     v_scale[page, head, place] = vs
 
 
-def attention(q, k, v, scale, causal, score_error=None):
+def attention(q, k, v, scale, causal, score_error=None, which=None):
     """One sequence: q [n, Hq, D], k and v [L, Hkv, D] float64.
 
     Returns out [n, Hq, D], lse [n, Hq], and for tolerances the sum of the
     terms' magnitudes mag = sum p |v| / sum p [n, Hq, D], and how far out and
     lse move at most, in first order, where the score of query (i, j) with
     token t is off by score_error(i, j, s) [seen] at most: p errs by the
-    factor of it in numerator and denominator.
+    factor of it in numerator and denominator.  which: the queries whose rows
+    are computed (all, if None).
     """
     n, Hq, D = q.shape
     L, Hkv, _ = k.shape
     out, mag, lse = np.zeros((n, Hq, D)), np.zeros((n, Hq, D)), np.full((n, Hq), -np.inf)
     out_off, lse_off = np.zeros((n, Hq, D)), np.zeros((n, Hq))
-    for i in range(n):
+    for i in range(n) if which is None else which:
         seen = max(0, L - n + i + 1) if causal else L
         if seen == 0:
             continue

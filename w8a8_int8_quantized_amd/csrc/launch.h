@@ -130,11 +130,11 @@ struct KvArgs {
   const int32_t* slots;
   uint8_t *k, *v;
   float *ks, *vs;
-  int64_t T, H, T4;               // T4: set by the launcher
+  int64_t T, H;
   int page, slots_end;            // slots_end: pages * page
 };
 constexpr int64_t kKvMaxHeads = 4096, kKvMaxPage = 1 << 20, kKvMaxRows = 1 << 27;   // rows: T * H
-hipError_t launch_kv(KvArgs a, bool write, int dtype, int bits, int D, hipStream_t st);
+hipError_t launch_kv(const KvArgs& a, bool write, int dtype, int bits, int D, hipStream_t st);
 
 // Attention over that cache (attn.hip); q_starts and lse may be null.
 // attn_workspace gives the workspace's size from a->sh and sets what depends
