@@ -268,14 +268,18 @@ class Problem:
 
 
 FORMS = [(64, 4), (128, 4), (256, 4), (64, 8), (128, 8), (256, 8)]
+# A block table that is wider than short segments may be: they are shared out
+# over workgroups then, and each by a workgroup of its own otherwise.
+WIDE = 2000
 LENGTHS = [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 95, 130, 257]
 
 
+@pytest.mark.parametrize("spare", [1, WIDE])
 @pytest.mark.parametrize("dt", [BF, FP])
 @pytest.mark.parametrize("D,bits", FORMS)
-def test_single_tokens_of_every_length(D, bits, dt):
-    print(f"attn lengths D={D} bits={bits} {dt}", flush=True)
-    p = Problem([(1, L) for L in LENGTHS] + [(1, 0)], 6, 2, D, bits, 16, dt, seed=D + bits)
+def test_single_tokens_of_every_length(D, bits, dt, spare):
+    print(f"attn lengths D={D} bits={bits} {dt} spare={spare}", flush=True)
+    p = Problem([(1, L) for L in LENGTHS] + [(1, 0)], 6, 2, D, bits, 16, dt, seed=D + bits, spare=spare)
     out, lse = p.call(ragged=False, lse=True)
     print("share of the tolerance", p.check(out, lse))
     assert not out[-1].any() and torch.isneginf(lse[-1]).all()
@@ -284,10 +288,12 @@ def test_single_tokens_of_every_length(D, bits, dt):
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (5, 5), (4, 2), (24, 3), (17, 1), (40, 1)])
 @pytest.mark.parametrize("D,bits", [(64, 4), (128, 4), (256, 4), (128, 8)])
-def test_head_layouts_and_query_tokens(D, bits, Hq, Hkv, causal):
-    print(f"attn heads {Hq}/{Hkv} D={D} bits={bits} causal={causal}", flush=True)
+@pytest.mark.parametrize("spare", [1, WIDE])
+def test_head_layouts_and_query_tokens(D, bits, Hq, Hkv, causal, spare):
+    print(f"attn heads {Hq}/{Hkv} D={D} bits={bits} causal={causal} spare={spare}", flush=True)
     lens = [(3, 40), (1, 77), (0, 50), (9, 9), (6, 2), (1, 0), (4, 0), (20, 133)]
-    p = Problem(lens, Hq, Hkv, D, bits, 32, BF if Hq % 2 else FP, seed=Hq, first_row=2, behind=3)
+    p = Problem(lens, Hq, Hkv, D, bits, 32, BF if Hq % 2 else FP, seed=Hq, first_row=2, behind=3,
+                spare=spare)
     i32 = p.q.shape[0], Hq
     out = torch.full((*i32, D), 7.5, dtype=p.dt, device=DEV)
     lse = torch.full(i32, 7.5, device=DEV)
@@ -381,7 +387,7 @@ def test_cache_beyond_four_gigabytes(bits):
 
 def test_calls_on_two_streams_at_once():
     """Each with a workspace of its own, the same cache read by both."""
-    p = Problem([(1, 5000), (1, 300), (1, 2222)], 8, 2, 128, 4, 64, BF, seed=12)
+    p = Problem([(1, 5000), (1, 300), (1, 2222)], 8, 2, 128, 4, 64, BF, seed=12, spare=WIDE)
     i32 = {"dtype": torch.int32, "device": DEV}
     args = (p.q.to(DEV), p.cache, torch.tensor(p.table, **i32), torch.tensor([L for _, L in p.lens], **i32))
     want = w8.attn_kv_cache(*args, lse=True)
@@ -409,7 +415,8 @@ def test_drawn_shapes(seed):
         lens.append((int(rng.integers(0, 1 + min(L, 30))) if rng.random() < 0.5 else 1, L))
     causal, dt = bool(rng.integers(0, 2)), (BF, FP)[int(rng.integers(0, 2))]
     print(f"attn drawn {lens} {Hkv}x{G} D={D} bits={bits} page={page} causal={causal} {dt}", flush=True)
-    p = Problem(lens, Hkv * G, Hkv, D, bits, page, dt, seed=seed, q_scale=float(np.exp(rng.normal())), spread=0.3)
+    p = Problem(lens, Hkv * G, Hkv, D, bits, page, dt, seed=seed, q_scale=float(np.exp(rng.normal())), spread=0.3,
+                spare=(1, WIDE)[seed % 2])
     scale = float(rng.uniform(0.02, 0.3))
     out, lse = p.call(lse=True, causal=causal, scale=scale)
     p.check(out, lse, causal=causal, scale=scale, sample=8)
@@ -417,10 +424,12 @@ def test_drawn_shapes(seed):
 
 @pytest.mark.parametrize("D,bits", FORMS)
 @pytest.mark.parametrize("q_scale,spread", [(30.0, 0.0), (0.0, 0.0), (1.0, 3.0), (8.0, 1.5)])
-def test_scores_and_scales_of_all_sizes(D, bits, q_scale, spread):
+@pytest.mark.parametrize("G,spare", [(2, 1), (2, WIDE), (3, WIDE), (6, 1), (6, WIDE)])
+def test_scores_and_scales_of_all_sizes(D, bits, q_scale, spread, G, spare):
     """Scores that rise by hundreds, none at all, scales that differ by orders of magnitude."""
-    print(f"attn q_scale={q_scale} spread={spread} D={D} bits={bits}", flush=True)
-    p = Problem([(1, 700), (2, 64), (1, 333)], 4, 2, D, bits, 64, BF, seed=7, q_scale=q_scale, spread=spread)
+    print(f"attn q_scale={q_scale} spread={spread} D={D} bits={bits} G={G} spare={spare}", flush=True)
+    p = Problem([(1, 700), (2, 64), (1, 333)], 2 * G, 2, D, bits, 64, BF, seed=7, q_scale=q_scale, spread=spread,
+                spare=spare)
     out, lse = p.call(lse=True)
     print("share of the tolerance", p.check(out, lse))
 
@@ -468,10 +477,11 @@ def test_strided_queries_scale_and_out():
     p.check(out, scale=-0.2)
 
 
-def test_entries_and_lengths_that_contradict_the_sizes():
+@pytest.mark.parametrize("pages", [0, 2, 300])
+def test_entries_and_lengths_that_contradict_the_sizes(pages):
     """Other sequences are as they would be, and nothing else is written."""
     lens = [(1, 100), (1, 50), (1, 40), (1, 64)]
-    p = Problem(lens, 4, 2, 128, 4, 32, BF, seed=4, behind=1)
+    p = Problem(lens, 4, 2, 128, 4, 32, BF, seed=4, behind=1, spare=pages)
     table = torch.tensor(p.table, device=DEV)
     table[0, 1], table[0, 2] = 1 << 30, -(1 << 31)
     kv = torch.tensor([100, 2 ** 31 - 1, -2 ** 31, 64], dtype=torch.int32, device=DEV)
@@ -483,16 +493,18 @@ def test_entries_and_lengths_that_contradict_the_sizes():
     p.call(q_starts=starts, max_q=2, out=out)
 
 
-def test_deterministic_and_independent_of_the_batch():
-    p = Problem([(1, 3000), (1, 700), (3, 1200)], 8, 4, 128, 4, 64, BF, seed=5)
+@pytest.mark.parametrize("spare", [1, WIDE])
+def test_deterministic(spare):
+    p = Problem([(1, 3000), (1, 700), (3, 1200)], 8, 4, 128, 4, 64, BF, seed=5, spare=spare)
     a = p.call(lse=True)
     for _ in range(3):
         assert _same(a, p.call(lse=True))
 
 
-def test_streams_workspace_and_capture():
+@pytest.mark.parametrize("spare", [1, WIDE])
+def test_streams_workspace_and_capture(spare):
     """A captured call replayed over new contents, on another stream, with a workspace of its own."""
-    p = Problem([(1, 400), (1, 1300)], 8, 2, 128, 4, 64, BF, seed=6)
+    p = Problem([(1, 400), (1, 1300)], 8, 2, 128, 4, 64, BF, seed=6, spare=spare)
     q = p.q.to(DEV)
     ws = torch.empty(w8.attn_workspace_bytes(1, 8, 2, 128), dtype=torch.uint8, device=DEV)
     ws.random_()

@@ -184,7 +184,7 @@ __device__ __forceinline__ uint32_t less(uint32_t h, float by) {
 }
 
 // --------------------------------------------------------------- one segment
-template <bool FP16, int D, int BITS, int ROWS>
+template <bool FP16, int D, int BITS, int ROWS, bool WHOLE>
 struct Attn {
   static constexpr int R = ROWS > 16 ? ROWS / 16 : 1;      // row fragments of 16 columns
   // Up to 4 or 8 rows leave most of a fragment's columns empty.  The scores of
@@ -216,8 +216,11 @@ struct Attn {
   // 4 KB or less.
   static constexpr int kDepth = kDB == 32 ? 4 : 2;
   static constexpr int kRingBytes = kDepth * kTileBytes;
-  static constexpr int kJoinBytes = kAttnWaves * kRound * 4 * 64 * 4;
-  static constexpr int kLdsBytes = kAttnWaves * kRingBytes > kJoinBytes ? kAttnWaves * kRingBytes : kJoinBytes;
+  // Waves to a workgroup; one that takes whole segments (short ones) has as
+  // many as LDS holds rings for.
+  static constexpr int kWaves = WHOLE ? attn_whole_waves(kDB) : kAttnWaves;
+  static constexpr int kJoinBytes = kWaves * kRound * 4 * 64 * 4;
+  static constexpr int kLdsBytes = kWaves * kRingBytes > kJoinBytes ? kWaves * kRingBytes : kJoinBytes;
 
   struct State {
     v4f o[R][kJ];
@@ -609,14 +612,17 @@ __device__ __forceinline__ v2f* piece_ml(const AttnArgs& a, uint32_t x, int row)
   return reinterpret_cast<v2f*>(a.part_ml) + (int64_t)x * ROWS + row;
 }
 
-template <bool FP16, int D, int BITS, int ROWS>
-__global__ __launch_bounds__(64 * kAttnWaves, 2) void k_attn(AttnArgs a) {
-  using A = Attn<FP16, D, BITS, ROWS>;
+// WHOLE: a workgroup to a segment, blockIdx.x counting sequence, row tile of
+// max_q tokens, key head; otherwise the workgroup's share of all segments.
+template <bool FP16, int D, int BITS, int ROWS, bool WHOLE>
+__global__ __launch_bounds__((64 * Attn<FP16, D, BITS, ROWS, WHOLE>::kWaves), WHOLE ? 1 : 2) void k_attn(AttnArgs a) {
+  using A = Attn<FP16, D, BITS, ROWS, WHOLE>;
+  constexpr int kWaves = A::kWaves;
   constexpr int R = A::R;
   __shared__ __align__(16) uint8_t ring[A::kLdsBytes];
   float* const lds = reinterpret_cast<float*>(ring);
   __shared__ __align__(16) uint8_t query[A::kQueryLds ? A::kQueryBytes : 16];
-  __shared__ float ldm[kAttnWaves][A::kRows], ldl[kAttnWaves][A::kRows];
+  __shared__ float ldm[kWaves][A::kRows], ldl[kWaves][A::kRows];
   __shared__ uint32_t red[kAttnWaves + kAttnFound];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, col = lane & 15;
@@ -627,24 +633,48 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_attn(AttnArgs a) {
   const uint8_t* const mine = ring + wave * A::kRingBytes;
   const uint32_t mine_at = lds_addr(mine);
 
-  const AttnFind f = find_units(a, blockIdx.x, red);
-  const uint32_t lo = blockIdx.x * f.share, hi = lo + f.share < f.total ? lo + f.share : f.total;
+  uint32_t u = 0, hi = 1, base = 0, share = 0;
+  int b, h_whole = 0, rt_whole = 0;
+  AttnSeq sq;
+  if constexpr (WHOLE) {
+    const uint32_t nrt = (uint32_t)(((int64_t)a.sh.max_q * a.sh.G + ROWS - 1) / ROWS), at = blockIdx.x / (uint32_t)a.sh.Hkv;
+    h_whole = (int)(blockIdx.x - at * a.sh.Hkv);
+    b = (int)(at / nrt);
+    rt_whole = (int)(at - b * nrt);
+    sq = get_seq(a, b);
+    if ((int64_t)rt_whole * ROWS >= (int64_t)sq.n * a.sh.G) return;
+  } else {
+    const AttnFind f = find_units(a, blockIdx.x, red);
+    share = f.share;
+    u = blockIdx.x * share;
+    hi = u + share < f.total ? u + share : f.total;
+    b = f.b;
+    base = f.base;
+    sq = f.sq;
+  }
   AttnSplit split = {};
 
-  int b = f.b;
-  uint32_t base = f.base;
-  AttnSeq sq = f.sq;
-  for (uint32_t u = lo; u < hi;) {
-    const AttnHead hd = attn_head(a.sh, sq);
-    const uint32_t units = (uint32_t)a.sh.Hkv * hd.units;
-    if (u >= base + units) {
-      base += units;
-      sq = get_seq(a, ++b);
-      continue;
+  while (u < hi) {
+    AttnSeg sg;
+    if constexpr (WHOLE) {
+      sg.tiles = sg.last = attn_tiles(a.sh, sq, (uint32_t)rt_whole);
+      sg.first = 0;
+      sg.h = h_whole;
+      sg.row_0 = (uint32_t)rt_whole * ROWS;
+      sg.rows = (uint32_t)sq.n * (uint32_t)a.sh.G;
+      u = hi;
+    } else {
+      const AttnHead hd = attn_head(a.sh, sq);
+      const uint32_t units = (uint32_t)a.sh.Hkv * hd.units;
+      if (u >= base + units) {
+        base += units;
+        sq = get_seq(a, ++b);
+        continue;
+      }
+      sg = attn_segment(a.sh, sq, hd, u - base, hi - base);
+      u += sg.units;
+      if (sg.first == sg.last) continue;
     }
-    const AttnSeg sg = attn_segment(a.sh, sq, hd, u - base, hi - base);
-    u += sg.units;
-    if (sg.first == sg.last) continue;
     const uint32_t tiles = sg.tiles, first = sg.first, last = sg.last, row_0 = sg.row_0, rows = sg.rows;
     const int h = sg.h;
     // the tokens that the first row sees, and all others then; tiles that see nothing are not computed
@@ -652,7 +682,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_attn(AttnArgs a) {
     const uint32_t row_last = row_0 + A::kRows < rows ? row_0 + A::kRows - 1 : rows - 1;
     const bool nothing = attn_seen(a.sh, sq, (int)(row_last / (uint32_t)a.sh.G)) == 0;
     const uint32_t count = nothing ? 0 : last - first;
-    const uint32_t per = (count + kAttnWaves - 1) / kAttnWaves;
+    const uint32_t per = (count + kWaves - 1) / kWaves;
     const uint32_t t0 = first + wave * per, end = first + count, t1 = t0 + per < end ? t0 + per : end;
 
     // The wave's tiles one behind the other, in half tiles of 16 tokens (which
@@ -737,10 +767,10 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_attn(AttnArgs a) {
       // (every wave has all of it, for c0)
 #pragma unroll
       for (int i = 0; i < R * A::kSteps; ++i)
-        if (i % kAttnWaves == wave) *reinterpret_cast<v4u*>(query + 1024 * i + 16 * lane) = qf[i / A::kSteps][i % A::kSteps];
+        if (i % kWaves == wave) *reinterpret_cast<v4u*>(query + 1024 * i + 16 * lane) = qf[i / A::kSteps][i % A::kSteps];
 #pragma unroll
       for (int r = 0; r < R; ++r)
-        if (r % kAttnWaves == wave)
+        if (r % kWaves == wave)
           *reinterpret_cast<v4f*>(query + 1024 * (R * A::kSteps + r) + 16 * lane) = v4f{c0[r], c0[r], c0[r], c0[r]};
       __syncthreads();
     }
@@ -769,9 +799,9 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_attn(AttnArgs a) {
     }
 
     // the waves join: common references, then the sums through LDS
-    const bool whole = first == 0 && last == tiles;
+    const bool whole = WHOLE || (first == 0 && last == tiles);
     const uint32_t piece = attn_place(blockIdx.x, first == 0);
-    if (first == 0 && !whole) split = {attn_followers(tiles, last, f.share), row_0, rows, sq.row0, h};
+    if (first == 0 && !whole) split = {attn_followers(tiles, last, share), row_0, rows, sq.row0, h};
     float fw[R], M[R], Ls[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -786,10 +816,10 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_attn(AttnArgs a) {
     for (int r = 0; r < R; ++r) {
       M[r] = ldm[0][16 * r + own];
 #pragma unroll
-      for (int w = 1; w < kAttnWaves; ++w) M[r] = fmaxf(M[r], ldm[w][16 * r + own]);
+      for (int w = 1; w < kWaves; ++w) M[r] = fmaxf(M[r], ldm[w][16 * r + own]);
       Ls[r] = 0.f;
 #pragma unroll
-      for (int w = 0; w < kAttnWaves; ++w) Ls[r] += ldl[w][16 * r + own] * exp2_hw(ldm[w][16 * r + own] - M[r]);
+      for (int w = 0; w < kWaves; ++w) Ls[r] += ldl[w][16 * r + own] * exp2_hw(ldm[w][16 * r + own] - M[r]);
       fw[r] = exp2_hw(st.m[r] - M[r]);
       if (whole) fw[r] = Ls[r] > 0.f ? fw[r] / Ls[r] : 0.f;
     }
@@ -805,15 +835,15 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_attn(AttnArgs a) {
       }
       __syncthreads();
 #pragma unroll
-      for (int n = 0; n < kN; n += 2 * kAttnWaves) {
+      for (int n = 0; n < kN; n += 2 * kWaves) {
         const int nn = n + 2 * wave;
-        if (kN < 2 * kAttnWaves && nn >= kN) continue;
+        if (kN < 2 * kWaves && nn >= kN) continue;
         v4f sum[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           sum[e] = *reinterpret_cast<const v4f*>(&lds[((nn + e) * 64 + lane) * 4]);
 #pragma unroll
-          for (int w = 1; w < kAttnWaves; ++w)
+          for (int w = 1; w < kWaves; ++w)
             sum[e] += *reinterpret_cast<const v4f*>(&lds[((w * A::kRound + nn + e) * 64 + lane) * 4]);
         }
         const int r = (n0 + nn) / A::kJ, j = (n0 + nn) % A::kJ;
@@ -840,7 +870,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_attn(AttnArgs a) {
     }
     __syncthreads();   // LDS is free for the next segment
   }
-  if (threadIdx.x == 0) static_cast<AttnSplit*>(a.splits)[blockIdx.x] = split;
+  if (!WHOLE && threadIdx.x == 0) static_cast<AttnSplit*>(a.splits)[blockIdx.x] = split;
 }
 
 // The segments that more than one workgroup holds: workgroup w joins the one
@@ -900,11 +930,18 @@ __global__ __launch_bounds__(SPREAD ? 512 : 256) void k_attn_join(AttnArgs a) {
 
 template <bool FP16, int D, int BITS, int ROWS>
 hipError_t attn_go(const AttnArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((k_attn<FP16, D, BITS, ROWS>), dim3((unsigned)a.workgroups), dim3(64 * kAttnWaves), 0, st, a);
+  const int64_t segments = (int64_t)a.sh.B * a.sh.Hkv * (((int64_t)a.sh.max_q * a.sh.G + ROWS - 1) / ROWS);
+  if constexpr (ROWS <= 16) {
+    if (attn_takes_whole(a.sh, segments, D * BITS / 8)) {
+      hipLaunchKernelGGL((k_attn<FP16, D, BITS, ROWS, true>), dim3((unsigned)segments),
+                         dim3(64 * attn_whole_waves(D * BITS / 8)), 0, st, a);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((k_attn<FP16, D, BITS, ROWS, false>), dim3((unsigned)a.workgroups), dim3(64 * kAttnWaves), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.workgroups == 1) return e;
   // many pieces to a segment where there are few segments
-  const int64_t segments = (int64_t)a.sh.B * a.sh.Hkv * (((int64_t)a.sh.max_q * a.sh.G + ROWS - 1) / ROWS);
   constexpr int kAcc = (ROWS > 16 ? ROWS / 16 : 1) * D / 16;
   if (segments * 4 <= a.workgroups)
     hipLaunchKernelGGL((k_attn_join<FP16, D, ROWS, true>),

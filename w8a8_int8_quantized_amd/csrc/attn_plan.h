@@ -152,6 +152,26 @@ W8_HD AttnSeg attn_segment(const AttnShape& a, const AttnSeq& s, const AttnHead&
   return g;
 }
 
+// Short segments are not shared: a workgroup of more waves to each, without a
+// search and without a second kernel (which also saves its launch on the
+// host).  The waves whose rings of two or four tiles fit in LDS, for rows of db
+// bytes.
+constexpr W8_HD int attn_whole_waves(int db) { return db <= 64 ? 16 : db == 128 ? 8 : 4; }
+
+// Segments that many, of which none is longer than the block table is wide.  A
+// few can be spread over the GPU, so their waves' runs have to be short; with
+// more than a workgroup to a CU the wide workgroups wait for each other.
+// Measured, us whole and shared, 128 channels of 4 bits: 8 segments of 1000
+// tokens 10.8 and 12.1, of 1500 12.5 and 12.0, of 2000 14.4 and 12.4; 64 of 2200
+// 17.1 and 17.2, of 3400 20.5 and 18.6; 128 of 1500 13.8 and 18.4, of 3500 20.9
+// and 23.2; 256 of 1200 14.4 and 20.4, of 3400 25.1 and 30.8; 512 of 500 17.4 and
+// 17.8, of 1500 29 and 24.
+W8_HD bool attn_takes_whole(const AttnShape& a, int64_t segments, int db) {
+  const int64_t most = ((int64_t)a.max_pages * a.page + kAttnTile - 1) / kAttnTile;
+  const int64_t run = segments <= 128 ? 3 + segments / 32 : segments <= 256 ? 7 : segments <= 512 ? 1 : 0;
+  return most <= run * attn_whole_waves(db);
+}
+
 // A segment of `tiles` tiles of which the workgroup that takes the first ends
 // with `last`: the workgroups that take the others, one behind the other.
 W8_HD uint32_t attn_followers(uint32_t tiles, uint32_t last, uint32_t share) {
