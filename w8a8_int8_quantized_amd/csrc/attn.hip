@@ -198,7 +198,6 @@ struct Attn {
   static constexpr int kSteps = D / 32;             // matrix instructions per half tile of S^T
   static constexpr int kJ = D / 16;                 // channels of a sixteenth: accumulators of O^T
   static constexpr int kRows = ROWS;
-  static constexpr int kRegs = R * kJ * 4;          // accumulator registers of a lane
   static constexpr int kRound = 8;                  // accumulators (of 4) per round through LDS
   // With more than one row fragment the query operand and the accumulators'
   // starting values lie in LDS, one copy to the workgroup: the registers hold
