@@ -514,7 +514,7 @@ int moe_w8a8_block(const int8_t* A, const float* a_scale, const int32_t* topk_id
  * dequant_kv_cache reads rows back, out[t] = q * s in fp32, rounded once:
  *   k, v     [T][Hkv][D] out, bf16, fp16 or fp32 (dtype), contiguous; tokens
  *            whose slot lies outside give zeros.  Slots may repeat.
- * T * Hkv <= 2^27.
+ * T * Hkv <= 2^27, Hkv counted up to a multiple of 4.
  */
 int quant_kv_cache(const void* k, const void* v, int dtype, int64_t k_stride,
                    int64_t v_stride, const int32_t* slots, int64_t T, int64_t Hkv,

@@ -491,6 +491,10 @@ static int check_kv_pointers(const void* k, const float* ks, const void* v, cons
   return aligned(k, 16) && aligned(ks, 16) && aligned(v, 16) && aligned(vs, 16) ? W8_OK : W8_ERR_ALIGN;
 }
 
+// Tokens to a write or read: workgroups have lanes for four heads each, and a
+// launch holds fewer than 2^32 lanes.
+static int64_t kv_most_tokens(int64_t Hkv) { return w8::kKvMaxRows / ((Hkv + 3) / 4 * 4); }
+
 // A stride between tokens whose rows are read 16 bytes at a time.
 static bool token_stride(int64_t s) { return s >= 0 && (s & 7) == 0 && s < kMaxElems; }
 
@@ -515,7 +519,7 @@ int quant_kv_cache(const void* k, const void* v, int dtype, int64_t k_stride, in
   if (dtype != W8_BF16 && dtype != W8_FP16) return W8_ERR_DTYPE;
   int rc = check_kv(Hkv, D, bits, pages, page_size);
   if (rc) return rc;
-  if (T < 0 || T > w8::kKvMaxRows / Hkv || !token_stride(k_stride) || !token_stride(v_stride)) return W8_ERR_SHAPE;
+  if (T < 0 || T > kv_most_tokens(Hkv) || !token_stride(k_stride) || !token_stride(v_stride)) return W8_ERR_SHAPE;
   if (T == 0) return W8_OK;
   if (!k || !v || !slots) return W8_ERR_NULL;
   rc = check_kv_pointers(k_cache, k_scale, v_cache, v_scale);
@@ -535,7 +539,7 @@ int dequant_kv_cache(const void* k_cache, const float* k_scale, const void* v_ca
   if (dtype != W8_BF16 && dtype != W8_FP16 && dtype != W8_FP32) return W8_ERR_DTYPE;
   int rc = check_kv(Hkv, D, bits, pages, page_size);
   if (rc) return rc;
-  if (T < 0 || T > w8::kKvMaxRows / Hkv) return W8_ERR_SHAPE;
+  if (T < 0 || T > kv_most_tokens(Hkv)) return W8_ERR_SHAPE;
   if (T == 0) return W8_OK;
   if (!k || !v || !slots) return W8_ERR_NULL;
   rc = check_kv_pointers(k_cache, k_scale, v_cache, v_scale);

@@ -133,7 +133,7 @@ struct KvArgs {
   int64_t T, H;
   int page, slots_end;            // slots_end: pages * page
 };
-constexpr int64_t kKvMaxHeads = 4096, kKvMaxPage = 1 << 20, kKvMaxRows = 1 << 27;   // rows: T * H
+constexpr int64_t kKvMaxHeads = 4096, kKvMaxPage = 1 << 20, kKvMaxRows = 1 << 27;   // rows: T * H, H counted up to fours
 hipError_t launch_kv(const KvArgs& a, bool write, int dtype, int bits, int D, hipStream_t st);
 
 // Attention over that cache (attn.hip); q_starts and lse may be null.
