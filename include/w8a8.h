@@ -558,7 +558,8 @@ int dequant_kv_cache(const void* k_cache, const float* k_scale, const void* v_ca
  * token may be anything, NaN among it.  Lengths and starts that contradict the
  * sizes are clamped to them, and table entries outside 0 .. pages - 1 read as
  * some page: unspecified values, no out-of-bounds access.
- * Hq is a multiple of Hkv, Hq <= 4096; max_q <= T;
+ * Hq is a multiple of Hkv, Hq <= 4096; max_q <= T; scale is finite, of any sign,
+ * and its product with log2(e) too (W8_ERR_VALUE);
  * B Hkv ceil(max_q Hq / Hkv / 16) ceil(max_pages page_size / 32) < 2^31.
  * Nothing is allocated; the call can be captured into a graph.
  */

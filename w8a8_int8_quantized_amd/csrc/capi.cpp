@@ -582,8 +582,9 @@ int attn_kv_cache(const void* q, int dtype, int64_t q_stride, const void* k_cach
   if (!token_stride(q_stride)) return W8_ERR_SHAPE;
   if (!q_starts && T != B * max_q) return W8_ERR_SHAPE;
   if (max_pages * page_size > kMaxRows) return W8_ERR_SHAPE;
-  // written so that a NaN fails
-  if (!(scale >= -3.4e38f && scale <= 3.4e38f)) return W8_ERR_VALUE;
+  // in base 2, as the kernels take it; written so that a NaN fails
+  const float scale_log2 = (float)(scale * 1.4426950408889634);
+  if (!(scale_log2 >= -3.4e38f && scale_log2 <= 3.4e38f)) return W8_ERR_VALUE;
   if (B == 0 || T == 0 || max_q == 0) return W8_OK;
   // the units of work stay inside 32 bits whatever the arrays hold
   const int64_t row_tiles = (max_q * (Hq / Hkv) + 15) / 16, tiles = (max_pages * page_size + 31) / 32 + 1;
@@ -616,7 +617,7 @@ int attn_kv_cache(const void* q, int dtype, int64_t q_stride, const void* k_cach
   a.sh.max_pages = (int)max_pages;
   a.sh.causal = causal != 0;
   a.pages = (int)pages;
-  a.scale_log2 = (float)(scale * 1.4426950408889634);
+  a.scale_log2 = scale_log2;
   if (workspace_bytes < w8::attn_workspace(&a, D, workspace)) return W8_ERR_WORKSPACE;
   return status_of(w8::launch_attn(a, dtype == W8_FP16, bits, (int)D, as_stream(stream)));
 }
