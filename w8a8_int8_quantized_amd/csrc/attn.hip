@@ -50,7 +50,7 @@
 // kernel alone, 94 now; other steps lie between).  Prompts: the vector pipe,
 // which takes the codes apart and does the softmax (by counters, 470 vector
 // instructions for 64 matrix ones, 64 rows of 32 tokens): 2048 tokens on 8192
-// take 306 us, 785 TFLOP/s, where a large bf16 library product reaches 1219.  Few
+// take 306 to 310 us, 780 TFLOP/s, where a large bf16 library product does 1219.  Few
 // tokens: a chain of loads (lengths, page ids and queries, tiles) and, where
 // segments are shared, the second kernel (5 to 7 us traced).
 #include "attn_plan.h"
