@@ -554,7 +554,10 @@ int dequant_kv_cache(const void* k_cache, const float* k_scale, const void* v_ca
  *            streams, or graphs that may run at the same time, need one each.
  * Scores, exponentials and sums are fp32; q enters exactly; p times the value
  * scale is rounded to fp16 (relative to the largest so far) for the second
- * product; out is rounded once.  Codes and scales behind a sequence's last
+ * product; out is rounded once.  Scores may be as large as fp32 holds: one that
+ * overflows in base 2 (s log2(e)) weighs nothing below the range and gives NaN
+ * above it, and scale ks log2(e) and 1152 sum_d |q[d]| have to be finite in fp32.
+ * Codes and scales behind a sequence's last
  * token may be anything, NaN among it.  Lengths and starts that contradict the
  * sizes are clamped to them, and table entries outside 0 .. pages - 1 read as
  * some page: unspecified values, no out-of-bounds access.

@@ -35,7 +35,11 @@
 // tile), so the accumulators are seldom rescaled.  p vs goes into the second
 // product as fp16: half a step is 2^-11 of the term, and what lies 2^-24 below
 // the largest is rounded to that.  References, l and all sums are fp32; the
-// reference cancels in o = O / l.
+// reference cancels in o = O / l.  Where scores pass 2^20 a step of fp32 is too
+// coarse for a reference that also holds the 2^10 and the scale: such rows take
+// a way of their own (far_references), which ordinary ones pay for with a
+// compare where references move and one a tile (0 to 1 % of a call, 2 % with 8
+// bits in 64 rows).
 //
 // Work is shared out in equal runs of 32-token tiles over all sequences and
 // heads (attn_plan.h); the waves of a workgroup take parts of a segment's run
@@ -68,7 +72,8 @@ typedef float v2f __attribute__((ext_vector_type(2)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
-constexpr float kUnset = -1e30f;          // a reference before the first score
+constexpr float kUnset = -3.4028235e38f;  // a reference before the first score: the least number
+constexpr float kFar = 1048576.f;         // 2^20: references from here on keep their lift apart
 constexpr float kLift = 10.f;             // log2 of what the largest p vs becomes
 constexpr float kTermLimit = 32768.f;     // what p vs may grow to: fp16 ends at 65504
 constexpr float kSumLimit = 1.2676506e30f;   // what a sum of p may grow to within a tile, 2^100
@@ -80,7 +85,7 @@ __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2
 // ln(l 2^m): the exponents are added exactly before the logarithm's rounding.
 __device__ __forceinline__ float log_sum(float m, float l) {
   const float e = (float)__builtin_amdgcn_frexp_expf(l);
-  return l > 0.f ? kLn2 * ((m + e) + __log2f(__builtin_amdgcn_frexp_mantf(l))) : -__builtin_inff();
+  return l == 0.f ? -__builtin_inff() : kLn2 * ((m + e) + __log2f(__builtin_amdgcn_frexp_mantf(l)));
 }
 
 // Across the lanes of a row: lane ^ FROM, lane ^ 2 FROM, .. lane ^ 32.
@@ -236,6 +241,7 @@ struct Attn {
   struct State {
     v4f o[R][kJ];
     float m[R], l[R];
+    bool far;       // (of the wave) a row's reference passes kFar
   };
 
   static __device__ __forceinline__ v4f mma(const v4u& a, const v4u& b, const v4f& c) {
@@ -382,12 +388,61 @@ struct Attn {
     }
   }
 
+  // Row r's sums in units of another reference, m.
+  static __device__ __forceinline__ void move(int r, float m, float by, State& st) {
+    st.m[r] = m;
+    st.l[r] *= by;
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) st.o[r][j] *= by;
+  }
+
+  // The references of a tile with far scores.  There a step of fp32 is more than
+  // the powers of two that p vs has room for, and the fused product that an
+  // exponent begins with lies up to half a step beside its rounding.  So the
+  // products are rounded first, the reference is the largest score itself, and
+  // its lift (what takes the largest term to kLift) is kept apart, in LDS, and
+  // added to the difference.  A wave that has such a row comes here with all
+  // its tiles.  m: the new references, by: what takes the sums to them; s f -
+  // ref become the exponents.
+  static __device__ __forceinline__ void far_references(float (*s)[kPer], float* f, const float* vs, float* lifts,
+                                                        float* m, float* by, float* ref, State& st) {
+    int at = (int)threadIdx.x & (ROWS < 16 ? ROWS - 1 : 15);
+    asm volatile("" : "+v"(at));   // (computed here, not held through the loop over the tiles)
+    bool far = false;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float top = -__builtin_inff(), e = -__builtin_inff();
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        s[r][i] *= f[i];
+        top = fmaxf(top, s[r][i]);
+      }
+      top = row_max<16 / PK>(top);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) e = fmaxf(e, (s[r][i] - top) + __log2f(fmaxf(vs[i], kTinyScale)));
+      const float to = kLift - row_max<16 / PK>(e), was = st.far ? lifts[16 * r + at] : 0.f;
+      // up from m - was to top - to
+      const bool up = (top - st.m[r]) + (was - to) > 0.f, apart = __builtin_fabsf(top) >= kFar;
+      const float lift = up ? (apart ? to : 0.f) : was;
+      m[r] = up ? (apart ? top : top - to) : st.m[r];
+      by[r] = up ? exp2_hw((st.m[r] - m[r]) + (lift - was)) : 1.f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) s[r][i] = (s[r][i] - m[r]) + lift;
+      ref[r] = 0.f;
+      far |= up && apart;
+      lifts[16 * r + at] = lift;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) f[i] = 1.f;
+    st.far |= __builtin_amdgcn_readfirstlane((int)(__ballot(far) != 0)) != 0;
+  }
+
   // The probabilities of tokens t0 .. t0 + 31 of the sequence, times the value
   // scales, as fp16.  seen: the keys that the lane's rows see; all: whether
-  // every row sees the whole tile.
+  // every row sees the whole tile.  lifts: of the wave's rows, in LDS.
   static __device__ __forceinline__ void softmax(const uint8_t* tile, const Lane& l, const v4f (*sc)[2],
-                                                 float scale_log2, int t0, bool all, int L, const int* seen, State& st,
-                                                 v4u* pf) {
+                                                 float scale_log2, int t0, bool all, int L, const int* seen,
+                                                 float* lifts, State& st, v4u* pf) {
     // score i of the lane: token l.tok + (i & 3) of half tile i / 4
     float s[R][kPer], f[kPer], vs[kPer];
     if constexpr (kPer == 2) {
@@ -428,15 +483,16 @@ struct Attn {
     }
     float sum[R];
     uint32_t pair[R][kPer / 2];
-    auto probabilities = [&] {
+    // p = exp2(exponent(r, i)) of score i of row r
+    auto probabilities = [&](auto exponent) {
       float top = 0.f;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float part[kPer / 2];
 #pragma unroll
         for (int i = 0; i < kPer / 2; ++i) {
-          const float p0 = exp2_hw(__builtin_fmaf(s[r][2 * i], f[2 * i], -st.m[r]));
-          const float p1 = exp2_hw(__builtin_fmaf(s[r][2 * i + 1], f[2 * i + 1], -st.m[r]));
+          const float p0 = exp2_hw(exponent(r, 2 * i));
+          const float p1 = exp2_hw(exponent(r, 2 * i + 1));
           const v2f x = {p0 * vs[2 * i], p1 * vs[2 * i + 1]};
           top = fmaxf(top, fmaxf(x[0], x[1]));
           part[i] = p0 + p1;
@@ -448,24 +504,29 @@ struct Attn {
       }
       return top;
     };
-    bool over = probabilities() > kTermLimit;
+    bool over = probabilities([&](int r, int i) { return __builtin_fmaf(s[r][i], f[i], -st.m[r]); }) > kTermLimit;
 #pragma unroll
     for (int r = 0; r < R; ++r) over |= sum[r] > kSumLimit;
-    if (__builtin_expect(__builtin_amdgcn_readfirstlane((int)(__ballot(over) != 0)), 0)) {
+    if (__builtin_expect(__builtin_amdgcn_readfirstlane((int)(__ballot(over) != 0)) | st.far, 0)) {
       // the references move to the largest term so far
+      float m[R], by[R], ref[R];
+      bool far = false;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float em = -__builtin_inff();
 #pragma unroll
         for (int i = 0; i < kPer; ++i) em = fmaxf(em, s[r][i] * f[i] + __log2f(fmaxf(vs[i], kTinyScale)));
-        em = fmaxf(st.m[r], row_max<16 / PK>(em) - kLift);
-        const float by = exp2_hw(st.m[r] - em);
-        st.m[r] = em;
-        st.l[r] *= by;
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) st.o[r][j] *= by;
+        m[r] = ref[r] = fmaxf(st.m[r], row_max<16 / PK>(em) - kLift);
+        by[r] = exp2_hw(st.m[r] - m[r]);
+        far |= __builtin_fabsf(m[r]) >= kFar && m[r] != kUnset;
       }
-      (void)probabilities();
+      if (__builtin_expect(__builtin_amdgcn_readfirstlane((int)(__ballot(far) != 0)) | st.far, 0))
+        far_references(s, f, vs, lifts, m, by, ref, st);
+      __builtin_amdgcn_sched_barrier(0);   // (mixed with what follows, the products take more registers)
+#pragma unroll
+      for (int r = 0; r < R; ++r) move(r, m[r], by[r], st);
+      __builtin_amdgcn_sched_barrier(0);
+      (void)probabilities([&](int r, int i) { return __builtin_fmaf(s[r][i], f[i], -ref[r]); });
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -633,7 +694,7 @@ __global__ __launch_bounds__((64 * Attn<FP16, D, BITS, ROWS, WHOLE>::kWaves), WH
   __shared__ __align__(16) uint8_t ring[A::kLdsBytes];
   float* const lds = reinterpret_cast<float*>(ring);
   __shared__ __align__(16) uint8_t query[A::kQueryLds ? A::kQueryBytes : 16];
-  __shared__ float ldm[kWaves][A::kRows], ldl[kWaves][A::kRows];
+  __shared__ float ldm[kWaves][A::kRows], ldl[kWaves][A::kRows], lifts[kWaves][A::kRows];
   __shared__ uint32_t red[kAttnWaves + kAttnFound];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, col = lane & 15;
@@ -773,6 +834,7 @@ __global__ __launch_bounds__((64 * Attn<FP16, D, BITS, ROWS, WHOLE>::kWaves), WH
 #pragma unroll
       for (int j = 0; j < A::kJ; ++j) st.o[r][j] = v4f{0.f, 0.f, 0.f, 0.f};
     }
+    st.far = false;
     const uint8_t* const ql = query + 16 * lane;
     if constexpr (A::kQueryLds) {
       // (every wave has all of it, for c0)
@@ -797,7 +859,7 @@ __global__ __launch_bounds__((64 * Attn<FP16, D, BITS, ROWS, WHOLE>::kWaves), WH
       v4u pf[R];
       A::scores(tile, ln, qf, ql, c0, e, s);
       A::softmax(tile, ln, s, a.scale_log2, (int)t * kAttnTile, (int)(t + 1) * kAttnTile <= seen_least, sq.L, seen,
-                 st, pf);
+                 lifts[wave], st, pf);
       uint32_t w[2][A::kW];
       A::values_of(tile, ln, 0, w[0]);
       A::values_of(tile, ln, 1, w[1]);
@@ -807,6 +869,12 @@ __global__ __launch_bounds__((64 * Attn<FP16, D, BITS, ROWS, WHOLE>::kWaves), WH
       }
       A::template values<0>(w, pf, e, st);
       got = got == A::kRingBytes - A::kTileBytes ? 0 : got + A::kTileBytes;
+    }
+
+    // fp32 holds the sums without the lifts
+    if (__builtin_expect(st.far, 0)) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) A::move(r, st.m[r], exp2_hw(-lifts[wave][16 * r + own]), st);
     }
 
     // the waves join: common references, then the sums through LDS
@@ -832,7 +900,7 @@ __global__ __launch_bounds__((64 * Attn<FP16, D, BITS, ROWS, WHOLE>::kWaves), WH
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) Ls[r] += ldl[w][16 * r + own] * exp2_hw(ldm[w][16 * r + own] - M[r]);
       fw[r] = exp2_hw(st.m[r] - M[r]);
-      if (whole) fw[r] = Ls[r] > 0.f ? fw[r] / Ls[r] : 0.f;
+      if (whole) fw[r] = Ls[r] == 0.f ? 0.f : fw[r] / Ls[r];
     }
     constexpr int kAcc = R * A::kJ;
 #pragma unroll
@@ -933,7 +1001,7 @@ __global__ __launch_bounds__(SPREAD ? 512 : 256) void k_attn_join(AttnArgs a) {
     }
   }
   if (!there) return;
-  const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+  const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
   const int64_t orow = out_row(a, sp.row0, sp.h, row);
   uint16_t* out = static_cast<uint16_t*>(a.out) + orow * D;
 #pragma unroll
