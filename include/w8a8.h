@@ -557,10 +557,11 @@ int dequant_kv_cache(const void* k_cache, const float* k_scale, const void* v_ca
  * product; out is rounded once.  Scores may be as large as fp32 holds: one that
  * overflows in base 2 (s log2(e)) weighs nothing below the range and gives NaN
  * above it, and scale ks log2(e) and 1152 sum_d |q[d]| have to be finite in fp32.
- * Codes and scales behind a sequence's last
- * token may be anything, NaN among it.  Lengths and starts that contradict the
- * sizes are clamped to them, and table entries outside 0 .. pages - 1 read as
- * some page: unspecified values, no out-of-bounds access.
+ * Codes and scales behind a sequence's last token may be anything, NaN among
+ * it, and a token's scales that are not finite reach only the queries that see
+ * it.  Lengths and starts that contradict the sizes are clamped to them, and
+ * table entries outside 0 .. pages - 1 read as some page: unspecified values,
+ * no out-of-bounds access.
  * Hq is a multiple of Hkv, Hq <= 4096; max_q <= T; scale is finite, of any sign,
  * and its product with log2(e) too (W8_ERR_VALUE);
  * B Hkv ceil(max_q Hq / Hkv / 16) ceil(max_pages page_size / 32) < 2^31.

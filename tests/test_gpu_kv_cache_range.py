@@ -165,3 +165,31 @@ def test_a_score_past_the_range():
     want = p.vq[0][keep, 0] * p.vs[0][keep, :].astype(np.float64)
     assert np.allclose(_f64(out)[0, 1], want.mean(0), rtol=0, atol=2.0 ** -9 * np.abs(want).mean(0).max())
     assert abs(float(lse[0, 1]) / (-7 * 16 * 2.0 ** 100 * math.log(2)) - 1) < 4 * U32
+
+
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("D,bits", FORMS)
+@pytest.mark.parametrize("G,n,spare", [(1, 3, 1), (1, 3, WIDE), (2, 4, 1), (5, 3, WIDE), (3, 40, 1), (4, 530, 1), (4, 5100, 1)])
+def test_hidden_tokens_of_any_value(G, n, spare, D, bits, dt, bad):
+    """The last tokens' scales are infinite or NaN: queries before them do not see that, and lse never does."""
+    print(f"attn hidden values G={G} n={n} spare={spare} D={D} bits={bits} {dt} {bad}", flush=True)
+    L = n + 45
+    p = Problem([(n, L), (n, n)], 2 * G, 2, D, bits, 32, dt, seed=G + n, spare=spare)
+    want, want_lse = p.call(lse=True)
+    _, ks, _, vs = p.cache
+    for b, kv in enumerate((L, n)):
+        for t in (kv - 1, kv - 2):
+            at = int(p.table[b, t // 32]), slice(None), t % 32
+            vs[at] = bad
+            if t == kv - 1:
+                ks[at] = bad
+    out, lse = p.call(lse=True)
+    for b in range(2):
+        rows = slice(int(p.starts[b]), int(p.starts[b]) + n)
+        o, z, full = _f64(out[rows]), _f64(lse[rows]), _f64(want_lse[rows])
+        assert np.isfinite(o[:-2]).all() and not np.isfinite(o[-2:]).all(-1).any()
+        assert np.allclose(z[:-1], full[:-1], rtol=0, atol=1e-5 * (1 + np.abs(full).max()))
+        # the queries that see none of it: what they gave before, but for references that moved elsewhere
+        d = np.abs(o[:-2] - _f64(want[rows])[:-2])
+        assert (d <= 2 * torch.finfo(dt).eps * (1 + np.abs(o[:-2]))).all()

@@ -396,30 +396,40 @@ struct Attn {
     for (int j = 0; j < kJ; ++j) st.o[r][j] *= by;
   }
 
-  // The references of a tile with far scores.  There a step of fp32 is more than
-  // the powers of two that p vs has room for, and the fused product that an
-  // exponent begins with lies up to half a step beside its rounding.  So the
-  // products are rounded first, the reference is the largest score itself, and
-  // its lift (what takes the largest term to kLift) is kept apart, in LDS, and
-  // added to the difference.  A wave that has such a row comes here with all
-  // its tiles.  m: the new references, by: what takes the sums to them; s f -
-  // ref become the exponents.
-  static __device__ __forceinline__ void far_references(float (*s)[kPer], float* f, const float* vs, float* lifts,
-                                                        float* m, float* by, float* ref, State& st) {
+  // The references of a tile with far scores, or with value scales that are not
+  // finite.  m: the new references, by: what takes the sums to them; s f - ref
+  // become the exponents.
+  //
+  // At a far score a step of fp32 is more than the powers of two that p vs has
+  // room for, and the fused product that an exponent begins with lies up to half
+  // a step beside its rounding.  So the products are rounded first, the reference
+  // is the largest score itself, and its lift (what takes the largest term to
+  // kLift) is kept apart, in LDS, and added to the difference.  A wave that has
+  // such a row comes here with all its tiles.
+  //
+  // A scale that is not finite must not reach rows that do not see its token,
+  // and 0 times it would.  It becomes 0, and the rows that see it get NaN.
+  static __device__ __forceinline__ void rare_references(float (*s)[kPer], float* f, float* vs, float* lifts, float* m,
+                                                         float* by, float* ref, State& st) {
     int at = (int)threadIdx.x & (ROWS < 16 ? ROWS - 1 : 15);
     asm volatile("" : "+v"(at));   // (computed here, not held through the loop over the tiles)
     bool far = false;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float top = -__builtin_inff(), e = -__builtin_inff();
+      float top = -__builtin_inff(), e = -__builtin_inff(), sees = 0.f;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         s[r][i] *= f[i];
         top = fmaxf(top, s[r][i]);
+        if (!(__builtin_fabsf(vs[i]) < __builtin_inff()) && s[r][i] != -__builtin_inff()) sees = 1.f;
       }
       top = row_max<16 / PK>(top);
+      sees = row_max<16 / PK>(sees);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) e = fmaxf(e, (s[r][i] - top) + __log2f(fmaxf(vs[i], kTinyScale)));
+      for (int i = 0; i < kPer; ++i) {
+        const float v = __builtin_fabsf(vs[i]) < __builtin_inff() ? fmaxf(vs[i], kTinyScale) : kTinyScale;
+        e = fmaxf(e, (s[r][i] - top) + __log2f(v));
+      }
       const float to = kLift - row_max<16 / PK>(e), was = st.far ? lifts[16 * r + at] : 0.f;
       // up from m - was to top - to
       const bool up = (top - st.m[r]) + (was - to) > 0.f, apart = __builtin_fabsf(top) >= kFar;
@@ -431,9 +441,15 @@ struct Attn {
       ref[r] = 0.f;
       far |= up && apart;
       lifts[16 * r + at] = lift;
+      const float spoil = sees != 0.f ? __builtin_nanf("") : 1.f;
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) st.o[r][j] *= spoil;
     }
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) f[i] = 1.f;
+    for (int i = 0; i < kPer; ++i) {
+      f[i] = 1.f;
+      vs[i] = __builtin_fabsf(vs[i]) < __builtin_inff() ? vs[i] : 0.f;
+    }
     st.far |= __builtin_amdgcn_readfirstlane((int)(__ballot(far) != 0)) != 0;
   }
 
@@ -470,12 +486,14 @@ struct Attn {
         }
       }
     }
+    bool odd = false;
     if (!all) {
       // what lies behind a row's last key may be anything, NaN among it
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int tok = t0 + l.tok + 16 * (i >> 2) + (i & 3);
         vs[i] = tok < L ? vs[i] : 0.f;
+        odd |= !(__builtin_fabsf(vs[i]) < __builtin_inff());
 #pragma unroll
         for (int r = 0; r < R; ++r) s[r][i] = tok < seen[r] ? s[r][i] * f[i] : -__builtin_inff();
         f[i] = 1.f;
@@ -504,13 +522,13 @@ struct Attn {
       }
       return top;
     };
-    bool over = probabilities([&](int r, int i) { return __builtin_fmaf(s[r][i], f[i], -st.m[r]); }) > kTermLimit;
+    bool over = odd | (probabilities([&](int r, int i) { return __builtin_fmaf(s[r][i], f[i], -st.m[r]); }) > kTermLimit);
 #pragma unroll
     for (int r = 0; r < R; ++r) over |= sum[r] > kSumLimit;
     if (__builtin_expect(__builtin_amdgcn_readfirstlane((int)(__ballot(over) != 0)) | st.far, 0)) {
       // the references move to the largest term so far
       float m[R], by[R], ref[R];
-      bool far = false;
+      bool rare = odd;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float em = -__builtin_inff();
@@ -518,10 +536,10 @@ struct Attn {
         for (int i = 0; i < kPer; ++i) em = fmaxf(em, s[r][i] * f[i] + __log2f(fmaxf(vs[i], kTinyScale)));
         m[r] = ref[r] = fmaxf(st.m[r], row_max<16 / PK>(em) - kLift);
         by[r] = exp2_hw(st.m[r] - m[r]);
-        far |= __builtin_fabsf(m[r]) >= kFar && m[r] != kUnset;
+        rare |= __builtin_fabsf(m[r]) >= kFar && m[r] != kUnset;
       }
-      if (__builtin_expect(__builtin_amdgcn_readfirstlane((int)(__ballot(far) != 0)) | st.far, 0))
-        far_references(s, f, vs, lifts, m, by, ref, st);
+      if (__builtin_expect(__builtin_amdgcn_readfirstlane((int)(__ballot(rare) != 0)) | st.far, 0))
+        rare_references(s, f, vs, lifts, m, by, ref, st);
       __builtin_amdgcn_sched_barrier(0);   // (mixed with what follows, the products take more registers)
 #pragma unroll
       for (int r = 0; r < R; ++r) move(r, m[r], by[r], st);
