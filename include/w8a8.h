@@ -564,7 +564,9 @@ int dequant_kv_cache(const void* k_cache, const float* k_scale, const void* v_ca
  * no out-of-bounds access.
  * Hq is a multiple of Hkv, Hq <= 4096; max_q <= T; scale is finite, of any sign,
  * and its product with log2(e) too (W8_ERR_VALUE);
- * B Hkv ceil(max_q Hq / Hkv / 16) ceil(max_pages page_size / 32) < 2^31.
+ * Hkv (T Hq / Hkv / 16 + B) (ceil(max_pages page_size / 32) + 33) < 2^32 - 2^12
+ * (with min(.., B ceil(max_q Hq / Hkv / 16)) for the first bracket; where the
+ * kernels take 32 or 64 rows at a time, 2 or 4 times that).
  * Nothing is allocated; the call can be captured into a graph.
  */
 int64_t attn_workspace_bytes(int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D);

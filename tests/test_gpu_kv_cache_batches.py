@@ -1,0 +1,33 @@
+"""Batches of many sequences over the quantised cache, against the 64-bit
+oracle (tolerances: test_gpu_kv_cache.py)."""
+
+import numpy as np
+import pytest
+import torch
+
+import w8a8_int8_quantized_amd as w8
+from test_gpu_kv_cache import BF, DEV, FP, WIDE, Problem
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_one_piece_among_many_single_tokens_over_a_wide_table(dt):
+    """The batch times the piece times the table's width would pass 2^31 units; all tokens together do not."""
+    rng = np.random.default_rng(4)
+    lens = [(1, int(n)) for n in rng.integers(1, 300, 299)]
+    lens.insert(17, (1024, 1100))
+    p = Problem(lens, 8, 2, 128, 4, 512, dt, seed=4, spare=6000)
+    tiles = p.table.shape[1] * 512 // 32
+    assert 300 * 2 * 256 * tiles > 1 << 31
+    out, lse = p.call(lse=True)
+    p.check(out, lse, sample=12)
+    # starts that give every other sequence all rows: more units than are counted, and nothing is computed
+    T = p.q.shape[0]
+    assert 150 * 2 * (T * 4 // 32) * (tiles - T // 32) > 1 << 32
+    starts = torch.tensor([0, T] * 150 + [0], dtype=torch.int32, device=DEV)
+    far = torch.full((300,), 2 ** 31 - 1, dtype=torch.int32, device=DEV)
+    kept = torch.full_like(out, 7.5)
+    p.call(out=kept, q_starts=starts, max_q=T, lens=far)
+    assert (kept == 7.5).all()
+    assert torch.equal(p.call(), out)

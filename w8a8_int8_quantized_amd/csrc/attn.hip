@@ -628,22 +628,23 @@ __device__ __forceinline__ AttnFind find_units(const AttnArgs& a, uint32_t workg
   uint32_t sum = 0;
   for (int b = b0; b < b0 + per && b < a.sh.B; ++b) {
     sq = get_seq(a, b);
-    sum += attn_units(a.sh, sq);
+    sum = attn_add(sum, attn_units(a.sh, sq));
   }
   uint32_t in = sum;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const uint32_t o = __shfl_up(in, d, 64);
-    if ((tid & 63) >= d) in += o;
+    if ((tid & 63) >= d) in = attn_add(in, o);
   }
   if ((tid & 63) == 63) red[tid >> 6] = in;
   __syncthreads();
   AttnFind f = {};
 #pragma unroll
   for (int w = 0; w < kAttnWaves; ++w) {
-    if (w < (tid >> 6)) in += red[w];
-    f.total += red[w];
+    if (w < (tid >> 6)) in = attn_add(in, red[w]);
+    f.total = attn_add(f.total, red[w]);
   }
+  if (f.total > kAttnMostUnits) f.total = 0;   // contradictory starts: nothing is computed
   f.share = attn_share(f.total, a.workgroups);
   const uint32_t want = workgroup * f.share;
   if (want >= f.total) return f;

@@ -99,6 +99,24 @@ W8_HD AttnHead attn_head(const AttnShape& a, const AttnSeq& s) {
 }
 W8_HD uint32_t attn_units(const AttnShape& a, const AttnSeq& s) { return (uint32_t)a.Hkv * attn_head(a, s).units; }
 
+// Units of several sequences; more than 32 bits hold stay at the largest number,
+// which is only reached where starts contradict the call's sizes.
+W8_HD uint32_t attn_add(uint32_t a, uint32_t b) { return a + b < a ? ~0u : a + b; }
+
+// The units of a call's sequences at most, whatever its arrays hold within its
+// sizes: T query tokens in all fill T G / rows row tiles of a key head and
+// begin one more for each sequence, and each counts its start and the tiles of
+// the whole table (a pair's two up to 30 more than these, see attn_head).
+inline uint64_t attn_most_units(const AttnShape& a) {
+  const int64_t each = (int64_t)a.B * (((int64_t)a.max_q * a.G + a.rows - 1) / a.rows);
+  const int64_t all = (int64_t)a.T * a.G / a.rows + a.B;
+  const int64_t row_tiles = (each < all ? each : all) * a.Hkv;
+  if (row_tiles >> 36) return ~0ull;
+  return (uint64_t)row_tiles * (uint64_t)(((int64_t)a.max_pages * a.page + kAttnTile - 1) / kAttnTile + 33);
+}
+// What the kernels count up to (and a share more than that).
+constexpr uint64_t kAttnMostUnits = 0xfffff000u;
+
 // Units to a workgroup: an even share, but two tiles to a wave at least.
 W8_HD uint32_t attn_share(uint32_t total, uint32_t workgroups) {
   const uint32_t even = (total + workgroups - 1) / workgroups;

@@ -586,17 +586,23 @@ int attn_kv_cache(const void* q, int dtype, int64_t q_stride, const void* k_cach
   const float scale_log2 = (float)(scale * 1.4426950408889634);
   if (!(scale_log2 >= -3.4e38f && scale_log2 <= 3.4e38f)) return W8_ERR_VALUE;
   if (B == 0 || T == 0 || max_q == 0) return W8_OK;
-  // the units of work stay inside 32 bits whatever the arrays hold
-  const int64_t row_tiles = (max_q * (Hq / Hkv) + 15) / 16, tiles = (max_pages * page_size + 31) / 32 + 1;
-  if (B > kMaxRows / Hkv || B * Hkv > kMaxRows / row_tiles || B * Hkv * row_tiles > kMaxRows / (tiles + 32))
-    return W8_ERR_SHAPE;
+  w8::AttnArgs a = {};
+  a.sh.B = (int)B;
+  a.sh.T = (int)T;
+  a.sh.Hkv = (int)Hkv;
+  a.sh.G = (int)(Hq / Hkv);
+  a.sh.max_q = (int)max_q;
+  a.sh.page = (int)page_size;
+  a.sh.max_pages = (int)max_pages;
+  a.sh.causal = causal != 0;
+  const int64_t need = w8::attn_workspace(&a, D, workspace);
+  if (w8::attn_most_units(a.sh) > w8::kAttnMostUnits) return W8_ERR_SHAPE;
   if (!q || !kv_lens || !out || !workspace || (max_pages > 0 && !block_table)) return W8_ERR_NULL;
   rc = check_kv_pointers(k_cache, k_scale, v_cache, v_scale);
   if (rc) return rc;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(block_table, 4) || !aligned(kv_lens, 4) ||
       !aligned(q_starts, 4) || !aligned(workspace, 256))
     return W8_ERR_ALIGN;
-  w8::AttnArgs a = {};
   a.q = q;
   a.q_stride = q_stride;
   a.k = static_cast<const uint8_t*>(k_cache);
@@ -608,17 +614,9 @@ int attn_kv_cache(const void* q, int dtype, int64_t q_stride, const void* k_cach
   a.q_starts = q_starts;
   a.out = out;
   a.lse = lse;
-  a.sh.B = (int)B;
-  a.sh.T = (int)T;
-  a.sh.Hkv = (int)Hkv;
-  a.sh.G = (int)(Hq / Hkv);
-  a.sh.max_q = (int)max_q;
-  a.sh.page = (int)page_size;
-  a.sh.max_pages = (int)max_pages;
-  a.sh.causal = causal != 0;
   a.pages = (int)pages;
   a.scale_log2 = scale_log2;
-  if (workspace_bytes < w8::attn_workspace(&a, D, workspace)) return W8_ERR_WORKSPACE;
+  if (workspace_bytes < need) return W8_ERR_WORKSPACE;
   return status_of(w8::launch_attn(a, dtype == W8_FP16, bits, (int)D, as_stream(stream)));
 }
 
