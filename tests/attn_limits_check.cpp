@@ -70,8 +70,21 @@ static int units() {
   return 0;
 }
 
+// Short segments have a workgroup each: few enough for one launch, whatever the table's width.
+static int whole() {
+  int round = 0;
+  for (int pages = 0; pages < 300; pages += pages < 3 ? 1 : 33)
+    for (int db = 32; db <= 256; db *= 2)
+      for (int64_t segments = 1; segments < (int64_t)1 << 40; segments += 1 + segments / 7, ++round) {
+        const AttnShape a = {1, 1, 1, 1, 1, 32, pages, 1, 4};
+        if (attn_takes_whole(a, segments, db)) CHECK(segments * 64 * attn_whole_waves(db) < (int64_t)1 << 32);
+        if (pages == 0 && segments <= 512) CHECK(attn_takes_whole(a, segments, db));
+      }
+  return 0;
+}
+
 int main() {
-  if (units()) return 1;
+  if (units() || whole()) return 1;
   std::printf("ok\n");
   return 0;
 }

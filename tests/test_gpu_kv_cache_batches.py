@@ -31,3 +31,14 @@ def test_one_piece_among_many_single_tokens_over_a_wide_table(dt):
     p.call(out=kept, q_starts=starts, max_q=T, lens=far)
     assert (kept == 7.5).all()
     assert torch.equal(p.call(), out)
+
+
+def test_a_table_without_pages():
+    """Nothing to see for more sequences than have a workgroup each: zeros."""
+    B = 700
+    c = w8.kv_cache_empty(1, 2, 16, 64)
+    q = torch.randn(B, 8, 64, device=DEV).to(BF)
+    table = torch.empty(B, 0, dtype=torch.int32, device=DEV)
+    lens = torch.arange(B, dtype=torch.int32, device=DEV)
+    out, lse = w8.attn_kv_cache(q, c, table, lens, lse=True)
+    assert not out.any() and torch.isneginf(lse).all()

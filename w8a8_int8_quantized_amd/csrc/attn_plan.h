@@ -187,7 +187,7 @@ constexpr W8_HD int attn_whole_waves(int db) { return db <= 64 ? 16 : db == 128 
 W8_HD bool attn_takes_whole(const AttnShape& a, int64_t segments, int db) {
   const int64_t most = ((int64_t)a.max_pages * a.page + kAttnTile - 1) / kAttnTile;
   const int64_t run = segments <= 128 ? 3 + segments / 32 : segments <= 256 ? 7 : segments <= 512 ? 1 : 0;
-  return most <= run * attn_whole_waves(db);
+  return segments <= 512 && most <= run * attn_whole_waves(db);   // (a table without pages has none)
 }
 
 // A segment of `tiles` tiles of which the workgroup that takes the first ends
