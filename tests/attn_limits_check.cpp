@@ -83,8 +83,30 @@ static int whole() {
   return 0;
 }
 
+// Sequences up to the longest: no sum leaves its type (built with checks for that).
+static int longest() {
+  const int round = 0;
+  for (int page = 16; page <= 1 << 20; page *= 2) {
+    const int pages = 2147483647 / page;
+    for (int back = 0; back < 100; ++back) {
+      for (int causal = 0; causal < 2; ++causal) {
+        const AttnShape a = {1, 50, 1, 3, 50, page, pages, causal, 16};
+        const AttnSeq s = attn_seq(a, 0, 50, pages * page - back);
+        CHECK(s.L == pages * page - back && s.n == 50);
+        const int last = attn_seen(a, s, 49);
+        const uint32_t tiles = attn_tiles(a, s, 9);
+        CHECK(last == s.L && tiles == ((uint64_t)last + 31) / 32);
+        for (uint32_t t = tiles - 3; t < tiles; ++t) CHECK(attn_tile_full(t, last) == ((uint64_t)t * 32 + 32 <= (uint64_t)last));
+        CHECK(attn_units(a, s) <= attn_most_units(a));
+      }
+    }
+  }
+  CHECK(!attn_tile_full(0, 0) && !attn_tile_full(0, 31) && attn_tile_full(0, 32));
+  return 0;
+}
+
 int main() {
-  if (units() || whole()) return 1;
+  if (units() || whole() || longest()) return 1;
   std::printf("ok\n");
   return 0;
 }

@@ -877,7 +877,7 @@ __global__ __launch_bounds__((64 * Attn<FP16, D, BITS, ROWS, WHOLE>::kWaves), WH
       v4f s[R][2];
       v4u pf[R];
       A::scores(tile, ln, qf, ql, c0, e, s);
-      A::softmax(tile, ln, s, a.scale_log2, (int)t * kAttnTile, (int)(t + 1) * kAttnTile <= seen_least, sq.L, seen,
+      A::softmax(tile, ln, s, a.scale_log2, (int)t * kAttnTile, attn_tile_full(t, seen_least), sq.L, seen,
                  lifts[wave], st, pf);
       uint32_t w[2][A::kW];
       A::values_of(tile, ln, 0, w[0]);

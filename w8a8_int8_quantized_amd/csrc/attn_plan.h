@@ -71,8 +71,12 @@ W8_HD int attn_seen(const AttnShape& a, const AttnSeq& s, int i) {
 W8_HD uint32_t attn_tiles(const AttnShape& a, const AttnSeq& s, uint32_t rt) {
   const int64_t last = ((int64_t)(rt + 1) * a.rows - 1) / a.G;
   const int seen = attn_seen(a, s, last < s.n ? (int)last : s.n - 1);
-  return seen > 0 ? (uint32_t)(seen + kAttnTile - 1) / kAttnTile : 1u;
+  return seen > 0 ? ((uint32_t)seen + kAttnTile - 1) / kAttnTile : 1u;
 }
+
+// Whether `seen` tokens hold all of tile t.  (Lengths go to 2^31 - 16, so a
+// tile's end may be 2^31.)
+W8_HD bool attn_tile_full(uint32_t t, int seen) { return (t + 1) * (uint32_t)kAttnTile <= (uint32_t)seen; }
 
 // A key head of a sequence: its row tiles, the units of a pair of them, and
 // all its units.
