@@ -42,3 +42,14 @@ def test_a_table_without_pages():
     lens = torch.arange(B, dtype=torch.int32, device=DEV)
     out, lse = w8.attn_kv_cache(q, c, table, lens, lse=True)
     assert not out.any() and torch.isneginf(lse).all()
+
+
+def test_no_query_tokens_to_a_sequence():
+    """max_q = 0 leaves nothing of q to compute: refused, but where there is nothing anyway."""
+    c = w8.kv_cache_empty(3, 2, 16, 128)
+    q = torch.zeros(4, 8, 128, dtype=BF, device=DEV)
+    i = torch.zeros(5, dtype=torch.int32, device=DEV)
+    with pytest.raises(w8.W8Error):
+        w8.attn_kv_cache(q, c, i[:2].view(1, 2), i[:1], q_starts=i[:2], max_q=0)
+    assert w8.attn_kv_cache(q[:0], c, i[:2].view(1, 2), i[:1], q_starts=i[:2], max_q=0).shape == (0, 8, 128)
+    assert w8.attn_kv_cache(q[:0], c, i[:2].view(1, 2), i[:1], q_starts=i[:2]).shape == (0, 8, 128)

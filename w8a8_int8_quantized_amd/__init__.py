@@ -740,7 +740,10 @@ def attn_kv_cache(q, cache, block_table, kv_lens, q_starts=None, max_q=None, sca
     among them) in the pages block_table[b] (int32 [B, max_pages]).  Without
     q_starts every sequence has T / B query tokens; with q_starts int32 [B + 1]
     sequence b has the rows q_starts[b] .. q_starts[b + 1] - 1, max_q of them at
-    most (default T), and rows of no sequence are left as they were.  causal:
+    most (default T), and rows of no sequence are left as they were (without
+    out: uninitialised).  Tight bounds are faster: the kernel goes by max_q and by
+    the block table's width (32 requests of up to 1200 tokens 12.5 us, with the
+    default max_q or a table for 131072 tokens 17 us).  causal:
     query i of n sees the first kv_lens[b] - n + i + 1 tokens, otherwise all; one
     that sees none gives zeros and lse -inf.  scale: D ** -0.5 by default.
     Hq is a multiple of the cache's heads, whose query heads are neighbours.
@@ -763,6 +766,8 @@ def attn_kv_cache(q, cache, block_table, kv_lens, q_starts=None, max_q=None, sca
     if q_starts is not None:
         _like(q_starts, "q_starts", (B + 1,), torch.int32, dev)
         max_q = T if max_q is None else min(max_q, T)
+        if T and not max_q:
+            raise W8Error(f"attn_kv_cache: max_q is 0 for {T} query tokens")
     else:
         n = T // B if B else 0
         if n * B != T or max_q not in (None, n):
