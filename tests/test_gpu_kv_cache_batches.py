@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import w8a8_int8_quantized_amd as w8
-from test_gpu_kv_cache import BF, DEV, FP, WIDE, Problem
+from test_gpu_kv_cache import BF, DEV, FORMS, FP, WIDE, Problem
+from test_gpu_kv_cache_range import Exact
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +54,33 @@ def test_no_query_tokens_to_a_sequence():
         w8.attn_kv_cache(q, c, i[:2].view(1, 2), i[:1], q_starts=i[:2], max_q=0)
     assert w8.attn_kv_cache(q[:0], c, i[:2].view(1, 2), i[:1], q_starts=i[:2], max_q=0).shape == (0, 8, 128)
     assert w8.attn_kv_cache(q[:0], c, i[:2].view(1, 2), i[:1], q_starts=i[:2]).shape == (0, 8, 128)
+
+
+def _batch(seed):
+    """40 sequences, of which a few are long: 160 segments of four key heads, joined in order."""
+    rng = np.random.default_rng(seed)
+    lens = [int(n) for n in rng.integers(0, 60, 34)] + [2000, 1999, 1700, 33, 901, 2017]
+    rng.shuffle(lens)
+    # 16 units to a segment beside its tiles, and 512 workgroups: the long ones have several followers
+    units = sum(4 * (16 + max(1, -(-n // 32))) for n in lens)
+    assert 4 * len(lens) * 4 > 512 and units // 512 + 1 < 20
+    return lens
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("D,bits", FORMS)
+@pytest.mark.parametrize("G", [3, 4, 6])
+def test_single_tokens_joined_in_order(G, D, bits, dt):
+    """Row tiles of 4 and 8: a full decode batch, a wide table."""
+    p = Problem([(1, n) for n in _batch(G)], 4 * G, 4, D, bits, 32, dt, seed=D + G, spare=WIDE)
+    out, lse = p.call(lse=True)
+    print("share of the tolerance", p.check(out, lse))
+    assert all(torch.equal(a, b) for a, b in zip(p.call(lse=True), (out, lse)))
+
+
+@pytest.mark.parametrize("D,bits,dt", [(64, 8, BF), (128, 4, FP), (256, 4, BF)])
+@pytest.mark.parametrize("f", [2.0, 2.0 ** 60])
+def test_far_scores_joined_in_order(D, bits, dt, f):
+    """Rows that hold their lifts apart, in pieces."""
+    p = Exact([max(n, 1) for n in _batch(3)], 1, 4, 4, D, bits, dt, f, seed=2, spare=WIDE)
+    p.check(*p.call(True), causal=True, sample=0)

@@ -193,3 +193,28 @@ def test_hidden_tokens_of_any_value(G, n, spare, D, bits, dt, bad):
         # the queries that see none of it: what they gave before, but for references that moved elsewhere
         d = np.abs(o[:-2] - _f64(want[rows])[:-2])
         assert (d <= 2 * torch.finfo(dt).eps * (1 + np.abs(o[:-2]))).all()
+
+
+@pytest.mark.parametrize("mean", [0.0, 8.0])
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("D,bits", FORMS)
+def test_scores_themselves(D, bits, dt, mean):
+    """Sequences of one token: lse is the score.  Its tolerance as in test_gpu_kv_cache.py, but with what each form adds
+    to its codes (the largest of them there), for queries around 0 and around 8."""
+    p = Problem([(1, 1)] * 40, 16, 4, D, bits, 16, dt, seed=D + bits)
+    p.q = (p.q.float() + mean).to(dt)
+    out, lse = p.call(ragged=False, lse=True)
+    z, q = _f64(lse), _f64(p.q)
+    offset, top = {(4, FP): 72, (4, BF): 136, (8, FP): 1152, (8, BF): 128}[bits, dt], 7 if bits == 4 else 127
+    worst = worst_off = 0.0
+    for b in range(40):
+        for j in range(16):
+            h = j // 4
+            s = D ** -0.5 * (p.k[b][0, h] @ q[b, j])
+            qa = np.abs(q[b, j]).sum()
+            codes = offset * (qa + abs(q[b, j].sum())) + top * qa
+            # (and the logarithm of a sum that is one power of two: 4 u32 (|s| + 1))
+            bound = 6 * math.sqrt(D + 1) * U32 * codes * D ** -0.5 * p.ks[b][0, h] + U32 * (10 * abs(s) + 8)
+            worst, worst_off = max(worst, abs(z[b, j] - s) / bound), max(worst_off, abs(z[b, j] - s))
+            assert abs(z[b, j] - s) <= bound, (b, j, s, z[b, j])
+    print(f"scores D={D} bits={bits} {dt} mean={mean}: off by {worst_off:.2e} at most, {worst:.3f} of the tolerance")
