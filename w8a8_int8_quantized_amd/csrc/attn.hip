@@ -130,7 +130,7 @@ __device__ __forceinline__ void dma_word_at(const uint8_t* p, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, off"
                ::"s"(lds), "v"(p) : "memory", "m0");
 }
-// All but N of the wave's vector memory operations are done; its LDS reads are.
+// All but N of the wave's vector memory operations are done.
 template <int N>
 __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
@@ -1040,7 +1040,7 @@ hipError_t attn_go(const AttnArgs& a, hipStream_t st) {
   }
   hipLaunchKernelGGL((k_attn<FP16, D, BITS, ROWS, false>), dim3((unsigned)a.workgroups), dim3(64 * kAttnWaves), 0, st, a);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.workgroups == 1) return e;
+  if (e != hipSuccess) return e;
   // Many pieces to a segment where there are few segments.  Measured, us of a
   // call spread and in order: 8 segments of 8192 tokens 14.9 and 15.5, of 131072
   // 38.1 and 38.9, 64 of up to 4000 16.3 and 17.0; 512 of up to 16384 101.2 and
