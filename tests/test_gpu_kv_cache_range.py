@@ -34,7 +34,7 @@ ROWS = [(2, 1), (6, 1), (5, 3), (4, 530), (4, 5100)]
 class Exact:
     """Sequences of L tokens; scores in base 2 are f times whole numbers."""
 
-    def __init__(self, lens, n, G, Hkv, D, bits, dt, f, seed, spare=1, page=32):
+    def __init__(self, lens, n, G, Hkv, D, bits, dt, f, seed, spare=1, page=32, vs_to=10):
         rng = np.random.default_rng(seed)
         top = 7 if bits == 4 else 127
         offset = {(4, FP): 72, (4, BF): 136, (8, FP): 1152, (8, BF): 128}[bits, dt]
@@ -52,7 +52,7 @@ class Exact:
             kq = rng.integers(-1, 2, (L, Hkv, D))
             kq[..., 0] = top
             vq = rng.integers(-top, top + 1, (L, Hkv, D))
-            vs = np.exp2(rng.uniform(-20, 10, (L, Hkv))).astype(np.float32)
+            vs = np.exp2(rng.uniform(-20, vs_to, (L, Hkv))).astype(np.float32)
             for t in range(L):
                 for h in range(Hkv):
                     oc.put(c, self.table[b, t // page], t % page, h, kq[t, h], np.float32(0.125), vq[t, h], vs[t, h], bits)
@@ -218,3 +218,12 @@ def test_scores_themselves(D, bits, dt, mean):
             worst, worst_off = max(worst, abs(z[b, j] - s) / bound), max(worst_off, abs(z[b, j] - s))
             assert abs(z[b, j] - s) <= bound, (b, j, s, z[b, j])
     print(f"scores D={D} bits={bits} {dt} mean={mean}: off by {worst_off:.2e} at most, {worst:.3f} of the tolerance")
+
+
+@pytest.mark.parametrize("f", [0.25, 2.0, 2.0 ** 40])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("G,n,spare", [(2, 1, 1), (6, 1, WIDE), (5, 3, 1), (4, 530, 1), (4, 5100, 1)])
+def test_values_of_every_size(G, n, spare, bits, f):
+    """Value scales from 2^-20 to 2^99 side by side: probabilities are lost from 2^-36 of the largest on only."""
+    p = Exact([333, 64], n, G, 2, 128, bits, BF, f, seed=n, spare=spare, vs_to=99)
+    p.check(*p.call(False), causal=False, sample=6)
