@@ -18,17 +18,22 @@
 // sixteenth, and bytes of two tokens are joined by one byte permutation.
 //
 // Each wave streams its tiles through a ring of its own in LDS, filled by
-// direct-to-LDS loads that read memory in order: no registers and no barriers,
-// and a load is in flight while the tiles before it are computed.  Keys are
-// swizzled within a row on the way, so that the fragment reads meet no bank
-// conflicts.
+// direct-to-LDS loads that read memory in order: no registers and no barriers.
+// Keys are swizzled within a row on the way, so that the fragment reads meet no
+// bank conflicts.  One tile is in flight while the one before it is computed up
+// to its probabilities, whatever the ring's depth: the compiler waits for all
+// loads in front of the two page ids of the next tile, as the register that
+// holds them is loaded in a branch (`next` below).
 //
 // Codes to 16-bit floats: OR an exponent on top of the code bits in place,
 // which gives 2^k + code + offset exactly.  For the keys the constant is not
 // subtracted from each but once from the sum: the accumulators start at
 // -(2^k + offset) * sum_d q[d].  For the values it is subtracted (exact in
 // fp16): a running sum over a long cache must not carry an offset that is
-// larger than its result.
+// larger than its result.  The sum of a score does carry it: scores of ordinary
+// queries (around 0) are off by 1e-6 to 3e-5 for it, those of fp16 queries of
+// mean 8, with 256 channels of 4 bits, by up to 1.2e-3 (a subtraction per pair of
+// codes is 32 vector instructions a tile for it, and bf16 has no packed one).
 //
 // Softmax: a row's probabilities are exp2(s - m) with a reference m that the
 // largest term p vs passes by 2^10 to 2^15 before it moves (one compare a
@@ -37,9 +42,10 @@
 // the largest is rounded to that.  References, l and all sums are fp32; the
 // reference cancels in o = O / l.  Where scores pass 2^20 a step of fp32 is too
 // coarse for a reference that also holds the 2^10 and the scale: such rows take
-// a way of their own (far_references), which ordinary ones pay for with a
-// compare where references move and one a tile (0 to 1 % of a call, 2 % with 8
-// bits in 64 rows).
+// a way of their own (rare_references), as do value scales that are not finite.
+// Ordinary rows pay for it with a scalar test a tile and compares where
+// references move and in masked tiles (0 to 2 % of a call, 2 to 4 % with 8 bits
+// in 64 rows).
 //
 // Work is shared out in equal runs of 32-token tiles over all sequences and
 // heads (attn_plan.h); the waves of a workgroup take parts of a segment's run
@@ -47,16 +53,20 @@
 // a second kernel, in order, so results do not depend on timing.  Short
 // segments have a workgroup of up to 16 waves each, and no second kernel.
 //
-// What bounds it.  Decoding: HBM reads.  64 sequences of 1 to 16384 tokens (32
-// query heads on 8, 128 channels, 4 bits, 473 MB) take 97.4 us, 4.9 TB/s; of 98.9
-// us, the loads without the computation took 94.6 and the computation without
-// the loads 66.5.  Tiles in registers instead of the LDS ring took 134 us (the
-// kernel alone, 94 now; other steps lie between).  Prompts: the vector pipe,
-// which takes the codes apart and does the softmax (by counters, 470 vector
+// What bounds it.  Decoding: reads with one tile of each wave in flight.  64
+// sequences of 1 to 16384 tokens (32 query heads on 8, 128 channels, 4 bits, 473
+// MB) take 97 us, 4.9 TB/s, where pure reads reach 6.3; of 98.9 us, the loads
+// without the computation took 94.6, with that wait in them, and the computation
+// without the loads 66.5.  Tiles in registers instead of the LDS ring took 134 us
+// (the kernel alone, 94 now; other steps lie between).  Prompts: the vector pipe,
+// which takes the codes apart and does the softmax (by counters, 472 vector
 // instructions for 64 matrix ones, 64 rows of 32 tokens): 2048 tokens on 8192
-// take 306 to 310 us, 780 TFLOP/s, where a large bf16 library product does 1219.  Few
-// tokens: a chain of loads (lengths, page ids and queries, tiles) and, where
-// segments are shared, the second kernel (5 to 7 us traced).
+// take 311 us, 780 TFLOP/s, where a large bf16 library product does 1219.  With 128
+// channels of 4 bits in 64 rows 39 vector registers do not fit and lie in scratch
+// (36 with fp16), some of them read back in the tile loop; 52 of the 140 kernels
+// keep scalars in vector lanes.  Few tokens: a chain of loads (lengths, page ids
+// and queries, tiles) and, where segments are shared, the second kernel (5 to 7
+// us traced).
 #include "attn_plan.h"
 #include "common.h"
 #include "launch.h"
@@ -228,8 +238,8 @@ struct Attn {
   static constexpr int kHalf = 16 * kDB;
   static constexpr int kTileBytes = 4 * kHalf + 256;
   static constexpr int kLoads = 4 * kHalf / 1024 + 1;    // loads to a tile
-  // Tiles in flight to a wave.  (Three of 4 KB: 107 us where two took 105, and 16
-  // waves of three do not fit in LDS.)
+  // Tiles in a wave's ring.  (Three of 4 KB: 107 us where two took 105, with the
+  // wait in front of page ids in both, and 16 waves of three do not fit in LDS.)
   static constexpr int kDepth = kDB == 32 ? 4 : 2;
   static constexpr int kRingBytes = kDepth * kTileBytes;
   // Waves to a workgroup; one that takes whole segments (short ones) has as
@@ -777,9 +787,10 @@ __global__ __launch_bounds__((64 * Attn<FP16, D, BITS, ROWS, WHOLE>::kWaves), WH
     const uint32_t t0 = first + wave * per, end = first + count, t1 = t0 + per < end ? t0 + per : end;
 
     // The wave's tiles one behind the other, in half tiles of 16 tokens (which
-    // lie in one page).  The pages are in a register, 64 at a time: a page id
-    // costs a lane read, not a load between the tiles.  Behind the sequence's
-    // last page the last one is read again, and nothing of it counts.
+    // lie in one page).  The pages are in a register, 64 at a time, so that a page
+    // id costs a lane read (and a wait for all loads before it) in place of a load
+    // between the tiles.  Behind the sequence's last page the last one is read
+    // again, and nothing of it counts.
     const int32_t* table = a.table + (int64_t)b * a.sh.max_pages;
     const uint32_t page_last = ((uint32_t)sq.L - 1) / (uint32_t)page;
     uint32_t n = t0 * kAttnTile / (uint32_t)page, off = t0 * kAttnTile - n * page;
@@ -1084,7 +1095,10 @@ hipError_t attn_pick(const AttnArgs& a, int bits, hipStream_t st) {
 // 592, 387, 315.  256 channels leave registers for 16 rows only: 4 tokens of
 // 64 requests (2560) 63, 92, -.
 // 512 workgroups: two to a CU stream as fast as four (64 sequences of 8192:
-// 107 us with 512, 112 with 1024), and leave half the pieces.
+// 107 us with 512, 112 with 1024), and leave half the pieces.  Two do not fit with
+// 8 bits and 256 channels (133 KB of LDS) or 128 channels in 64 rows (91 KB):
+// these run in two rounds (2048 tokens on 8192 in 8 bits 551 to 557 us; one round of 256 was
+// not measured).
 int64_t attn_workspace(AttnArgs* a, int64_t D, void* ws) {
   const int64_t rows = (int64_t)a->sh.max_q * a->sh.G, all = (int64_t)a->sh.T * a->sh.Hkv * a->sh.G;
   a->sh.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 || D == 256 || all < 4096 ? 16 : rows <= 32 || all < 40000 ? 32 : 64;

@@ -187,7 +187,10 @@ constexpr W8_HD int attn_whole_waves(int db) { return db <= 64 ? 16 : db == 128 
 // tokens 10.8 and 12.1, of 1500 12.5 and 12.0, of 2000 14.4 and 12.4; 64 of 2200
 // 17.1 and 17.2, of 3400 20.5 and 18.6; 128 of 1500 13.8 and 18.4, of 3500 20.9
 // and 23.2; 256 of 1200 14.4 and 20.4, of 3400 25.1 and 30.8; 512 of 500 17.4 and
-// 17.8, of 1500 29 and 24.
+// 17.8, of 1500 29 and 24; nothing between 256 and 512.  The table's width stands
+// for the lengths, which are on the device: one that is wider than its sequences
+// need has them shared (32 of up to 1200 under a table for 131072 tokens 17 us,
+// 12.5 with one for 1200).
 W8_HD bool attn_takes_whole(const AttnShape& a, int64_t segments, int db) {
   const int64_t most = ((int64_t)a.max_pages * a.page + kAttnTile - 1) / kAttnTile;
   const int64_t run = segments <= 128 ? 3 + segments / 32 : segments <= 256 ? 7 : segments <= 512 ? 1 : 0;
