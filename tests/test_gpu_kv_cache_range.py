@@ -227,3 +227,23 @@ def test_values_of_every_size(G, n, spare, bits, f):
     """Value scales from 2^-20 to 2^99 side by side: probabilities are lost from 2^-36 of the largest on only."""
     p = Exact([333, 64], n, G, 2, 128, bits, BF, f, seed=n, spare=spare, vs_to=99)
     p.check(*p.call(False), causal=False, sample=6)
+
+
+@pytest.mark.parametrize("L", [1, 10, 40, 700])
+@pytest.mark.parametrize("D,bits", FORMS)
+@pytest.mark.parametrize("G", [2, 6, 12])
+@pytest.mark.parametrize("spare", [1, WIDE])
+def test_scores_above_the_range_give_nan(G, D, bits, L, spare):
+    """In out and in lse, whether one wave holds the sequence or many do; rows beside them are as ever."""
+    p = Exact([L], 1, G, 1, D, bits, FP, 2.0 ** 100, seed=L, spare=spare)
+    p.q[0, 1, 1:] = 0
+    p.q[0, 1, 0] = 16
+    t = L // 2
+    k = p.cache[1].clone()
+    k[p.table[0, t // 32], 0, t % 32] *= 2.0 ** 24     # that token's score: 16 * 7 (or 127) * 2^124
+    rest = [j for j in range(G) if j != 1]
+    p.q[0, rest] = 0
+    p.cache = (p.cache[0], k, *p.cache[2:])
+    out, lse = p.call(True)
+    assert torch.isnan(out[0, 1]).all() and torch.isnan(lse[0, 1])
+    assert torch.isfinite(out[0, rest]).all() and np.allclose(_f64(lse)[0, rest], math.log(L), rtol=0, atol=1e-5)

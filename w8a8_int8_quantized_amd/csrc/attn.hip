@@ -441,8 +441,8 @@ struct Attn {
         e = fmaxf(e, (s[r][i] - top) + __log2f(v));
       }
       const float to = kLift - row_max<16 / PK>(e), was = st.far ? lifts[16 * r + at] : 0.f;
-      // up from m - was to top - to
-      const bool up = (top - st.m[r]) + (was - to) > 0.f, apart = __builtin_fabsf(top) >= kFar;
+      // up from m - was to top - to (and to an infinite top, where the difference is NaN)
+      const bool up = !((top - st.m[r]) + (was - to) <= 0.f), apart = __builtin_fabsf(top) >= kFar;
       const float lift = up ? (apart ? to : 0.f) : was;
       m[r] = up ? (apart ? top : top - to) : st.m[r];
       by[r] = up ? exp2_hw((st.m[r] - m[r]) + (lift - was)) : 1.f;
