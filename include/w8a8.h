@@ -556,11 +556,11 @@ int dequant_kv_cache(const void* k_cache, const float* k_scale, const void* v_ca
  * scale is rounded to fp16 (relative to the largest so far) for the second
  * product; out is rounded once.  Scores may be as large as fp32 holds: one that
  * overflows in base 2 (s log2(e)) weighs nothing below the range (a query with no
- * other score is as one that sees nothing) and gives NaN above it, and scale ks log2(e) and 1152 sum_d |q[d]| have to be finite in fp32.
- * (Codes carry an offset of 72 to 1152 into a score's sum: queries far from 0 on
- * average cost it digits, 1e-3 for fp16 ones of mean 8 with 256 channels.)  Where
- * value scales pass 2^100, weights below 2^-36 of the largest (2^-15 at 2^121)
- * count as 0.
+ * other score is as one that sees nothing) and gives NaN above it; scale ks
+ * log2(e) and 1152 sum_d |q[d]| have to be finite in fp32.  Codes carry an offset
+ * of 72 to 1152 into a score's sum: queries far from 0 on average cost it digits
+ * (1e-3 for fp16 ones of mean 8 with 256 channels).  Where value scales pass
+ * 2^100, weights below 2^-36 of the largest (2^-15 at 2^121) count as 0.
  * Codes and scales behind a sequence's last token may be anything, NaN among
  * it, and a token's scales that are not finite reach only the queries that see
  * it.  Lengths and starts that contradict the sizes are clamped to them, and
